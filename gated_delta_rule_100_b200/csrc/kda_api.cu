@@ -23,6 +23,7 @@ cudaError_t launch_decode(const void *q, const void *k, const void *v, const flo
 #include "bwd_params.cuh"
 #include "chunk_common.cuh"
 #include "chunk_params.cuh"
+#include "kda_internal.cuh"
 
 namespace kda {
 cudaError_t launch_prep(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tg, const PrepParams &prm,
@@ -246,6 +247,20 @@ cudaError_t timed_launch(int dev, int kind, cudaStream_t s, F &&fn) {
     return e;
 }
 
+}  // namespace
+
+// What the other files of the C boundary share (kda_internal.cuh).
+namespace kda {
+int host_status_word(uint32_t **out) { return current_status_word(out); }
+int host_encoder(PFN_cuTensorMapEncodeTiled_v12000 *fn) { return get_encoder(fn); }
+uint64_t host_wait_polls() {
+    const unsigned long long polls = g_wait_polls.load();
+    return polls ? polls : ~0ull;
+}
+}  // namespace kda
+
+namespace {
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -276,6 +291,12 @@ int num_sms(int dev) {
     }
     return g_num_sms[dev];
 }
+
+}  // namespace
+namespace kda {
+int host_num_sms(int dev) { return num_sms(dev); }
+}  // namespace kda
+namespace {
 
 // Tensor maps over the record parts of `nrec` consecutive records at `rec`
 // (layouts in chunk_common.cuh), with the boxes and swizzles of the chain

@@ -1,0 +1,464 @@
+// paged_attn.cu -- attention of new tokens over a paged cache for few rows
+// (single tokens, a few drafted tokens, any page size), and the join of rows
+// whose keys were split.
+//
+// For token i of sequence n (n_q new tokens, cache length L with them), head h:
+//   o = sum_{j <= L - n_q + i} p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j)
+// in one pass over the keys with a running maximum m and sum l per row:
+//   m' = max(m, x),  o <- o 2^(m-m') + 2^(x-m') v,  l <- l 2^(m-m') + 2^(x-m').
+// Statistics and sums are fp32; the weights 2^(x-m) are rounded to the inputs'
+// 16-bit type as the operand of the second product (relative error at most half
+// a step each, and the roundings of many keys average out), while l sums them
+// before that rounding.
+//
+// Bound: HBM.  A key head's keys and values are read once for all its G query
+// heads and new tokens: 4 d bytes per key, against 4 d G n_q operations, far
+// under the card's ratio.  So the kernel is laid out for loads in flight: the
+// rows (tokens x G, at most 16 per item) fill the 16 rows of an mma.sync tile;
+// each of the four warps walks its own 16 keys of every 64 with its own ring of
+// asynchronous 16-byte copies and no block-wide barrier; rows out of the
+// sequence's end are filled with zeros, so whatever lies behind it (NaN too)
+// never meets the products.
+//
+// Work is cut into equal runs of 64-key units over all (sequence, key head, row
+// tile) items, one run per CTA: lengths from 1 to the cache's end load every SM
+// alike.  A run has at most one item that began before it and one that ends
+// after it; these write their sums to slots, joined by the second kernel in a
+// fixed order (no atomics, so results do not depend on timing).
+#include "paged_params.cuh"
+
+namespace kda {
+
+constexpr int PA_THREADS = 128, PA_WARPS = 4, PA_ROWS = 16, PA_UNIT = 64, PA_WKEYS = 16;
+
+template <int D>
+struct PaShape {
+    static constexpr int ROWB = D * 2;                        // bytes of a key
+    static constexpr int TILE = PA_WKEYS * ROWB;              // one warp's keys of a stage
+    static constexpr int STAGE = 2 * TILE;                    // keys and values
+    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int RING = STAGE * STAGES;               // per warp
+    static constexpr int MERGE = PA_WARPS * PA_ROWS * D * 4;  // fp32 sums, reusing the rings
+    static constexpr int SMEM = PA_WARPS * RING > MERGE ? PA_WARPS * RING : MERGE;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <bool BF>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 64-key units of row tile t.  A tile that sees nothing keeps one, so that its
+// rows are written.
+__device__ __forceinline__ int pa_units(const PagedSeq &s, int G, int t) {
+    return max(1, (paged_kv_end(s, G, (t + 1) * PA_ROWS - 1) + PA_UNIT - 1) / PA_UNIT);
+}
+__device__ __forceinline__ int pa_tiles(const PagedSeq &s, int G) { return (s.nq * G + PA_ROWS - 1) / PA_ROWS; }
+__device__ __forceinline__ long long pa_head_units(const PagedSeq &s, int G) {
+    long long w = 0;
+    const int tiles = pa_tiles(s, G);
+    for (int t = 0; t < tiles; ++t) w += pa_units(s, G, t);
+    return w;
+}
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParams p) {
+    using S = PaShape<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_sum[PA_WARPS];
+    __shared__ long long s_start;                 // first unit of the item found
+    __shared__ int s_n, s_h, s_t;
+    __shared__ float2 s_ml[PA_WARPS][PA_ROWS];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.G, c = blockIdx.x, grid = gridDim.x;
+    launch_dependents();
+
+    // ---- plan: the units of every sequence, and the item that this run begins in
+    const int per = (p.N + PA_THREADS - 1) / PA_THREADS;
+    long long mine = 0;
+    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) {
+        const PagedSeq s = paged_seq(p, n, c == 0);
+        mine += pa_head_units(s, G) * p.Hkv;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, W = 0;
+    for (int w = 0; w < PA_WARPS; ++w) {
+        if (w < warp) before += s_sum[w];
+        W += s_sum[w];
+    }
+    const long long runs = W < grid ? W : grid;  // every run has at least one unit
+    if (tid == 0) p.entries[c].count = 0;
+    if (c >= runs) return;
+    long long u = c * W / runs;
+    const long long u_end = (c + 1) * W / runs;
+    if (u >= before && u < before + mine) {      // exactly one thread
+        long long left = u - before, start = before;
+        int n = tid * per;
+        for (;; ++n) {
+            const PagedSeq s = paged_seq(p, n, false);
+            const long long hu = pa_head_units(s, G), w = hu * p.Hkv;
+            if (left >= w) { left -= w; start += w; continue; }
+            const int h = (int)(left / hu);
+            left -= h * hu;
+            start += h * hu;
+            int t = 0;
+            for (int k; left >= (k = pa_units(s, G, t)); ++t) { left -= k; start += k; }
+            s_n = n; s_h = h; s_t = t; s_start = start;
+            break;
+        }
+    }
+    __syncthreads();
+    int n = s_n, h = s_h, t = s_t;
+    long long start = s_start;                   // the item's first unit
+
+    const uint32_t ring = smem_u32(smem) + warp * S::RING;
+    const int g8 = lane >> 2, t4 = lane & 3;
+    PagedSeq s = paged_seq(p, n, false);
+
+    while (u < u_end) {
+        const int units = pa_units(s, G, t);
+        const int off = (int)(u - start);
+        const int cnt = (int)min((long long)(units - off), u_end - u);
+        const int rows = s.nq * G;
+        const int kv_end = paged_kv_end(s, G, (t + 1) * PA_ROWS - 1);
+        const int first_new = s.len - s.nq;      // may be negative: tokens without a place
+        const int *trow = p.table + (long long)s.row * p.P;
+
+        // the new tokens' keys and values of this run go to their pages; they are
+        // read below from where they came, so nothing waits for these stores
+        if (p.k_new != nullptr && t == 0) {
+            // (row tile 0's last unit writes what no unit of it covers: a tile sees at least the first token)
+            const int lo = max(max(off * PA_UNIT, first_new), 0);
+            const int hi = off + cnt == units ? s.len : min(s.len, (off + cnt) * PA_UNIT);
+            constexpr int CH = D / 8;
+            for (int i = tid; i < max(hi - lo, 0) * CH; i += PA_THREADS) {
+                const int pos = lo + i / CH, ch = i % CH, tok = s.q0 + pos - first_new;
+                const int page = trow[pos / p.page_size], in = pos % p.page_size;
+                if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
+                const uint4 kx = *reinterpret_cast<const uint4 *>(p.k_new + tok * p.kn_ts + h * D + ch * 8);
+                const uint4 vx = *reinterpret_cast<const uint4 *>(p.v_new + tok * p.vn_ts + h * D + ch * 8);
+                *reinterpret_cast<uint4 *>(p.kp + page * p.k_ps + in * p.k_ts + h * p.k_hs + ch * 8) = kx;
+                *reinterpret_cast<uint4 *>(p.vp + page * p.v_ps + in * p.v_ts + h * p.v_hs + ch * 8) = vx;
+            }
+        }
+
+        // ---- the warp's loads: 16 keys of each unit
+        const uint16_t *kptr = p.kp, *vptr = p.vp;
+        bool kvalid = false;
+        auto locate = [&](int step) {  // lane l < 16: where key l of the step lies
+            const int pos = (off + step) * PA_UNIT + warp * PA_WKEYS + (lane & 15);
+            kvalid = step < cnt && pos < kv_end;
+            kptr = p.kp;
+            vptr = p.vp;
+            if (kvalid) {
+                if (p.k_new != nullptr && pos >= first_new) {
+                    const long long tok = s.q0 + pos - first_new;
+                    kptr = p.k_new + tok * p.kn_ts + h * D;
+                    vptr = p.v_new + tok * p.vn_ts + h * D;
+                } else {
+                    const int page = trow[pos / p.page_size], in = pos % p.page_size;
+                    if (page >= 0 && page < p.num_pages) {
+                        kptr = p.kp + page * p.k_ps + in * p.k_ts + h * p.k_hs;
+                        vptr = p.vp + page * p.v_ps + in * p.v_ts + h * p.v_hs;
+                    } else {
+                        kvalid = false;
+                        report(p.st, DEV_BAD_ARG);
+                    }
+                }
+            }
+        };
+        auto issue = [&](int step) {
+            constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte pieces of a key, keys of one copy
+            const uint32_t kb = ring + (step % S::STAGES) * S::STAGE, vb = kb + S::TILE;
+            const int ch = lane % CPR;
+#pragma unroll
+            for (int i = 0; i < PA_WKEYS / RPI; ++i) {
+                const int r = i * RPI + lane / CPR;
+                const uint16_t *ks = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)kptr, r));
+                const uint16_t *vs = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)vptr, r));
+                const bool ok = __shfl_sync(0xffffffffu, (int)kvalid, r) != 0;
+                const uint32_t o = r * S::ROWB + ((ch ^ (r & 7)) << 4);
+                cp16(kb + o, ks + ch * 8, ok);
+                cp16(vb + o, vs + ch * 8, ok);
+            }
+        };
+        locate(0);
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; ++i) {
+            if (i < cnt) issue(i);
+            cp_commit();
+            locate(i + 1);
+        }
+
+        // ---- the rows' queries as mma operands, straight from memory
+        uint32_t qf[D / 16][4];
+        int qpos[2];  // last key that the thread's two rows see; -1: none
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = t * PA_ROWS + g8 + 8 * e;
+            const bool ok = r < rows;
+            qpos[e] = ok ? first_new + r / G : -1;
+            const uint16_t *qr = p.q + (ok ? (s.q0 + r / G) * p.q_ts + (long long)(h * G + r % G) * D : 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][e] = ok ? *reinterpret_cast<const uint32_t *>(qr + k * 16 + t4 * 2) : 0u;
+                qf[k][2 + e] = ok ? *reinterpret_cast<const uint32_t *>(qr + k * 16 + 8 + t4 * 2) : 0u;
+            }
+        }
+        const int low_pos = first_new + (t * PA_ROWS) / G;  // the smallest last key of the tile's rows
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        for (int step = 0; step < cnt; ++step) {
+            cp_wait<S::STAGES - 2>();
+            __syncwarp();
+            if (step + S::STAGES - 1 < cnt) issue(step + S::STAGES - 1);  // the stage read in the step before
+            cp_commit();
+            if (step + S::STAGES < cnt) locate(step + S::STAGES);
+            const uint32_t kb = ring + (step % S::STAGES) * S::STAGE, vb = kb + S::TILE;
+            const int base = (off + step) * PA_UNIT + warp * PA_WKEYS;
+            float x[2][4] = {};
+            {
+                const int r = (lane >> 4) * 8 + (lane & 7), hi = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t b[4];
+                    ldsm4(b, kb + r * S::ROWB + (((k * 2 + hi) ^ (r & 7)) << 4));
+                    mma16<BF>(x[0], qf[k], b[0], b[1]);
+                    mma16<BF>(x[1], qf[k], b[2], b[3]);
+                }
+            }
+            const bool all = base + PA_WKEYS - 1 <= low_pos;  // no row's mask reaches these keys
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = x[nt][e] * p.scale_log2;
+                    x[nt][e] = all || base + nt * 8 + t4 * 2 + (e & 1) <= qpos[e >> 1] ? y : -INFINITY;
+                }
+            float f[2];
+            uint32_t pa[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx, m[e]);
+                const float ref = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every weight is 2^-inf = 0
+                f[e] = ex2(m[e] - ref);
+                m[e] = mx;
+                float sum = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x[nt][2 * e + j] = ex2(x[nt][2 * e + j] - ref);
+                        sum += x[nt][2 * e + j];
+                    }
+                l[e] = l[e] * f[e] + sum;
+                pa[e] = pack16x2<BF>(x[0][2 * e], x[0][2 * e + 1]);
+                pa[2 + e] = pack16x2<BF>(x[1][2 * e], x[1][2 * e + 1]);
+            }
+            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= f[0]; o[i][1] *= f[0];
+                    o[i][2] *= f[1]; o[i][3] *= f[1];
+                }
+            }
+            {
+                const int r = ((lane >> 3) & 1) * 8 + (lane & 7), hi = lane >> 4;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];
+                    ldsm4t(b, vb + r * S::ROWB + (((i * 2 + hi) ^ (r & 7)) << 4));
+                    mma16<BF>(o[2 * i], pa, b[0], b[1]);
+                    mma16<BF>(o[2 * i + 1], pa, b[2], b[3]);
+                }
+            }
+        }
+        cp_wait<0>();
+
+        // ---- the four warps' sums, joined in shared memory
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (t4 == 0) s_ml[warp][g8 + 8 * e] = make_float2(m[e], l[e]);
+        }
+        __syncthreads();  // every warp is done with its ring
+        float *mo = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float2 *>(mo + (warp * PA_ROWS + g8 + 8 * e) * D + i * 8 + t4 * 2) =
+                    make_float2(o[i][2 * e], o[i][2 * e + 1]);
+        __syncthreads();
+        const bool begins = off == 0, ends = off + cnt == units;
+        const int slot = begins ? grid + c : c;
+#pragma unroll
+        for (int i = 0; i < PA_ROWS * D / 4 / PA_THREADS; ++i) {
+            const int at = i * PA_THREADS + tid, r = at / (D / 4), col = (at % (D / 4)) * 4;
+            float M = -INFINITY, L = 0.f;
+            for (int w = 0; w < PA_WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float ref = M == -INFINITY ? 0.f : M;
+            for (int w = 0; w < PA_WARPS; ++w) {
+                const float fw = ex2(s_ml[w][r].x - ref);
+                const float4 y = *reinterpret_cast<const float4 *>(mo + (w * PA_ROWS + r) * D + col);
+                L += fw * s_ml[w][r].y;
+                a.x += fw * y.x; a.y += fw * y.y; a.z += fw * y.z; a.w += fw * y.w;
+            }
+            const int row = t * PA_ROWS + r;
+            if (begins && ends) {
+                if (row < rows) {
+                    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+                    const long long tok = s.q0 + row / G;
+                    const int head = h * G + row % G;
+                    uint2 y;
+                    y.x = pack16x2<BF>(a.x * inv, a.y * inv);
+                    y.y = pack16x2<BF>(a.z * inv, a.w * inv);
+                    *reinterpret_cast<uint2 *>(p.out + (tok * p.Hq + head) * D + col) = y;
+                    if (p.lse != nullptr && col == 0)
+                        p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
+                }
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + ((long long)slot * PA_ROWS + r) * D + col) = a;
+                if (col == 0) p.part_ml[(long long)slot * PA_ROWS + r] = make_float2(M, L);
+            }
+        }
+        if (begins && !ends && tid == 0) {
+            // runs c + 1 .. last hold the rest: the last is the one with the item's last unit
+            const long long e = start + units;
+            const int last = (int)((e * runs + W - 1) / W) - 1;
+            p.entries[c] = {n, h, t, grid + c, c + 1, last - c};
+        }
+        __syncthreads();
+
+        u += cnt;
+        if (u < u_end) {  // the next item
+            start += units;
+            if (++t == pa_tiles(s, G)) {
+                t = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    do s = paged_seq(p, ++n, false); while (s.nq == 0);
+                }
+            }
+        }
+    }
+}
+
+// Joins the pieces of a split item: entry blockIdx.x, four rows per block, one
+// warp per row.  Reads each piece's row once; with the pieces of a run of CTAs
+// still in L2 it is bound by latency, so a lane keeps four loads in flight.
+template <int D, bool BF>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p, int tile_rows) {
+    wait_for_primary();
+    const SplitEntry e = p.entries[blockIdx.x];
+    if (e.count == 0) return;
+    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const PagedSeq s = paged_seq(p, e.n, false);
+    const int row = e.t * tile_rows + r;
+    if (r >= tile_rows || row >= s.nq * p.G) return;
+    auto slot = [&](int i) { return (long long)(i == 0 ? e.head : e.next + i - 1) * tile_rows + r; };
+    float M = -INFINITY;
+    for (int i = lane; i <= e.count; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.f : M;
+    constexpr int V = D / 32;
+    float a[V] = {}, L = 0.f;
+#pragma unroll 4
+    for (int i = 0; i <= e.count; ++i) {
+        const float2 ml = p.part_ml[slot(i)];
+        const float f = ex2(ml.x - ref);
+        L += f * ml.y;
+        const float *src = p.part_o + slot(i) * D + lane * V;
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 y = *reinterpret_cast<const float2 *>(src + j);
+            a[j] += f * y.x;
+            a[j + 1] += f * y.y;
+        }
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const long long tok = s.q0 + row / p.G;
+    const int head = e.h * p.G + row % p.G;
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+        *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + head) * D + lane * V + j) = pack16x2<BF>(a[j] * inv, a[j + 1] * inv);
+    if (p.lse != nullptr && lane == 0) p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
+}
+
+// ------------------------------------------------------------------- host ----
+int paged_rows_slots(int ctas) { return 2 * ctas; }
+int paged_rows_ctas_per_sm(int d) { return d == 128 ? 2 : 3; }
+int paged_rows_tile() { return PA_ROWS; }
+
+template <int D, bool BF>
+static cudaError_t launch_rows_t(const PagedParams &p, int ctas, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    paged_rows_kernel<D, BF><<<ctas, PA_THREADS, PaShape<D>::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+template <int D, bool BF>
+static cudaError_t launch_join_t(const PagedParams &p, int entries, int tile_rows, cudaStream_t stream) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(entries, (tile_rows + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF>, p, tile_rows);
+}
+
+cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, int ctas, cudaStream_t stream) {
+    if (d == 128) return bf ? launch_rows_t<128, true>(p, ctas, stream) : launch_rows_t<128, false>(p, ctas, stream);
+    return bf ? launch_rows_t<64, true>(p, ctas, stream) : launch_rows_t<64, false>(p, ctas, stream);
+}
+cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, int entries, int tile_rows, cudaStream_t stream) {
+    if (d == 128)
+        return bf ? launch_join_t<128, true>(p, entries, tile_rows, stream) : launch_join_t<128, false>(p, entries, tile_rows, stream);
+    return bf ? launch_join_t<64, true>(p, entries, tile_rows, stream) : launch_join_t<64, false>(p, entries, tile_rows, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,90 @@
+// paged_params.cuh -- what the paged-attention kernels share: their
+// parameters, the geometry of a sequence, and the join of split rows.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "kda_device.cuh"
+
+namespace kda {
+
+// One row's partial result over part of its keys: unnormalised sums against
+// the running maximum m (log2 units), l = sum of 2^(x - m).  The pieces of a
+// split item lie in slots of `rows` rows: `head`, then next .. next + count - 1.
+struct SplitEntry {
+    int n, h, t;     // sequence, key head, row tile
+    int head, next, count;  // count = 0: nothing to join
+};
+
+struct PagedParams {
+    const uint16_t *q, *k_new, *v_new;  // 16-bit [total_q][heads][d], token strides below
+    uint16_t *kp, *vp;                  // pages
+    const int *cu, *table, *length, *rows;
+    uint16_t *out;
+    float *lse;
+    float scale_log2;                   // scale * log2(e)
+    int N, total_q, max_q, Hq, Hkv, G, page_size, num_pages, P, R;
+    long long q_ts, kn_ts, vn_ts;       // elements between tokens
+    long long k_ps, k_ts, k_hs;         // key pages: elements between pages, tokens, heads
+    long long v_ps, v_ts, v_hs;         // value pages
+    float *part_o;                      // [slots][rows][d]
+    float2 *part_ml;                    // [slots][rows]
+    SplitEntry *entries;
+    DeviceStatus st;
+};
+
+// Sequence n of the batch, from arrays the host never reads: every value is
+// bounded here before it is used as an index, and a change is reported.
+struct PagedSeq {
+    int q0, nq, len, row;  // first token, new tokens, cache length with them, table row
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int n, bool tell) {
+    PagedSeq s;
+    const int a = p.cu[n], b = p.cu[n + 1];
+    s.row = p.rows != nullptr ? p.rows[n] : n;
+    const bool row_ok = s.row >= 0 && s.row < p.R;
+    if (!row_ok) s.row = 0;
+    const int len = row_ok ? p.length[s.row] : 0;
+    bool ok = row_ok && a >= 0 && b >= a && b <= p.total_q && b - a <= p.max_q && len >= 0 &&
+              (long long)len <= (long long)p.P * p.page_size;
+    s.q0 = min(max(a, 0), p.total_q);
+    s.nq = min(min(max(b, s.q0), p.total_q) - s.q0, p.max_q);
+    s.len = (int)min((long long)max(len, 0), (long long)p.P * p.page_size);
+    if (tell && !ok) report(p.st, DEV_BAD_ARG);
+    return s;
+}
+
+// Rows of a sequence are its tokens times the G query heads of one key head,
+// row r = token r / G, head r % G.  Keys that rows [0, r] see at most.
+__device__ __forceinline__ int paged_kv_end(const PagedSeq &s, int G, int last_row) {
+    const int r = min(last_row, s.nq * G - 1);
+    return max(0, s.len - s.nq + r / G + 1);
+}
+
+__device__ __forceinline__ uint16_t f32_to_16(float x, bool bf) {
+    if (bf) return to_bf16_bits(x);
+    const __half h = __float2half_rn(x);
+    return *reinterpret_cast<const uint16_t *>(&h);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
+    if constexpr (BF) return pack_bf16x2(lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 2^x by the hardware's unit (relative error about 2^-22); 2^-inf = 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float LN2 = 0.69314718055994531f;
+
+// Launch-order hints between a kernel and the one after it on the stream.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace kda

@@ -1,0 +1,444 @@
+// pages.cu -- the pages of a cache: reserve, fork, free, compact, copy.
+//
+// A cache is one or more pools of num_pages pages, a table [R][P] of page
+// numbers (row r holds the sequence in slot r, its first ceil(length[r] /
+// page_size) entries in use, -1 behind them), length[R], and ref[num_pages],
+// the number of rows that hold each page (0: free).
+//
+// Nothing here computes; each kernel's bound is the memory it touches, and for
+// the small ones the latency of a few dependent reads.  Pages are handed out
+// lowest number first, in the order of the caller's list, so results are the
+// same whatever the timing.  A call whose list is bad (a row out of range, a
+// row named twice, a length that shrinks or does not fit) changes nothing and is
+// reported; so is a reservation for which there are too few pages, through its
+// info word.
+#include <cooperative_groups.h>
+
+#include "pages_params.cuh"
+
+namespace kda {
+
+namespace cg = cooperative_groups;
+
+constexpr int PG_THREADS = 1024, PG_WARPS = PG_THREADS / 32, PG_CLUSTER = 8;
+
+// Exclusive prefix of v over the block, and the block's total.  sm: PG_WARPS + 1 ints.
+__device__ __forceinline__ int block_prefix(int v, int *sm, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    __syncthreads();  // sm may still be read from the call before
+    if (lane == 31) sm[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int x = lane < (int)blockDim.x / 32 ? sm[lane] : 0;
+        int y = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += up;
+        }
+        sm[lane] = y - x;
+        if (lane == 31) sm[32] = y;
+    }
+    __syncthreads();
+    total = sm[32];
+    return sm[warp] + incl - v;
+}
+
+__device__ __forceinline__ int pages_of(int len, int ps) { return (int)(((long long)len + ps - 1) / ps); }
+
+// Marks rows[0..n) in the bitmap; false where one is out of range or marked already.
+// Called by the whole block; needs a barrier before the bitmap is read.
+__device__ __forceinline__ bool mark_rows(const int *rows, int n, int R, uint32_t *bits) {
+    bool ok = true;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int r = rows[i];
+        if (r < 0 || r >= R) { ok = false; continue; }
+        const uint32_t b = 1u << (r & 31);
+        if (atomicOr(&bits[r >> 5], b) & b) ok = false;
+    }
+    return ok;
+}
+
+// ------------------------------------------------------------------- free ----
+// Every block checks the whole list (a few reads a thread), then takes rows in
+// turn, a warp a row.
+__global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
+    __shared__ uint32_t bits[PG_MAX_ROWS / 32];
+    for (int i = threadIdx.x; i < (p.R + 31) / 32; i += blockDim.x) bits[i] = 0;
+    __syncthreads();
+    const bool ok = mark_rows(p.rows, p.n, p.R, bits);
+    if (__syncthreads_or(!ok)) {
+        if (threadIdx.x == 0) report(p.st, DEV_BAD_ARG);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
+    for (int i = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.n; i += warps) {
+        const int row = p.rows[i];
+        int *tr = p.table + (long long)row * p.P;
+        const int len = p.length[row];
+        const int held = min(pages_of(max(len, 0), p.ps), p.P);
+        for (int j = lane; j < held; j += 32) {
+            const int page = tr[j];
+            tr[j] = -1;
+            if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
+            if (atomicSub(&p.ref[page], 1) <= 0) {  // held by nobody: the count stays at zero
+                atomicAdd(&p.ref[page], 1);
+                report(p.st, DEV_BAD_ARG);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) p.length[row] = 0;
+    }
+}
+
+// -------------------------------------------------------- reserve and fork ----
+// One cluster of eight CTAs, one launch: every CTA checks the list and sums the
+// pages that its sequences need, each counts the free pages of its eighth of
+// ref, the counts meet over distributed shared memory, and each hands out the
+// free pages of its own eighth: the f-th free page goes to the sequence whose
+// needs cover rank f.  Two passes over ref, the second from L2.
+struct GrantShared {
+    int sm[33];
+    uint32_t bits[PG_MAX_ROWS / 32];
+    int start[PG_MAX_LIST + 1];  // exclusive prefix of the sequences' needs
+    int warp_free[PG_WARPS];
+    int cta_free;
+};
+
+// Free flags of pages [4 i, 4 i + 4).
+__device__ __forceinline__ uint32_t free_nibble(const int *ref, int num_pages, int i) {
+    uint32_t m = 0;
+    if (4 * i + 3 < num_pages && (reinterpret_cast<uintptr_t>(ref) & 15u) == 0) {
+        const int4 x = *reinterpret_cast<const int4 *>(ref + 4 * i);
+        m = (x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3;
+    } else {
+        for (int k = 0; k < 4; ++k)
+            if (4 * i + k < num_pages && ref[4 * i + k] == 0) m |= 1u << k;
+    }
+    return m;
+}
+
+template <bool FORK>
+__global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS) pages_grant_kernel(const PagesParams p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    GrantShared &s = *reinterpret_cast<GrantShared *>(raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- the list: rows in range and named once; what each needs
+    for (int i = tid; i < (p.R + 31) / 32; i += PG_THREADS) s.bits[i] = 0;
+    __syncthreads();
+    bool ok = mark_rows(p.rows, p.n, p.R, s.bits);
+    __syncthreads();
+    int total = 0;
+    for (int base = 0; base < p.n; base += PG_THREADS) {
+        const int i = base + tid;
+        int need = 0;
+        if (i < p.n) {
+            const int row = p.rows[i];
+            if (row >= 0 && row < p.R) {
+                const int have = p.length[row];
+                if constexpr (FORK) {
+                    const int from = p.src[i];
+                    if (from < 0 || from >= p.R || (s.bits[from >> 5] >> (from & 31) & 1u) || have != 0) {
+                        ok = false;
+                    } else {
+                        const int len = p.length[from];
+                        if (len < 0 || pages_of(len, p.ps) > p.P) ok = false;
+                        else need = len % p.ps != 0;
+                    }
+                } else {
+                    const int want = p.new_length[i];
+                    if (have < 0 || want < have || pages_of(want, p.ps) > p.P) ok = false;
+                    else need = pages_of(want, p.ps) - pages_of(have, p.ps);
+                }
+            }
+        }
+        int sum;
+        const int at = block_prefix(need, s.sm, sum);
+        if (i < p.n) s.start[i] = total + at;
+        total += sum;  // at most the table's entries, which the host holds below 2^31
+    }
+    if (tid == 0) s.start[p.n] = total;
+    auto no_copies = [&]() {
+        if constexpr (FORK)
+            for (int i = cta * PG_THREADS + tid; i < p.n; i += PG_CLUSTER * PG_THREADS) p.copy_src[i] = p.copy_dst[i] = -1;
+    };
+    if (__syncthreads_or(!ok)) {  // the same in every CTA: all return before the cluster's barrier
+        if (tid == 0 && cta == 0) report(p.st, DEV_BAD_ARG);
+        no_copies();
+        return;
+    }
+
+    // ---- free pages of this CTA's eighth, a warp a contiguous run of 128-page steps
+    const int steps = (p.num_pages + 127) / 128, warps = PG_CLUSTER * PG_WARPS, gw = cta * PG_WARPS + warp;
+    const int s0 = (int)((long long)steps * gw / warps), s1 = (int)((long long)steps * (gw + 1) / warps);
+    int cnt = 0;
+#pragma unroll 8
+    for (int k = s0; k < s1; ++k) cnt += __popc(free_nibble(p.ref, p.num_pages, k * 32 + lane));
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) s.warp_free[warp] = cnt;
+    __syncthreads();
+    if (warp == 0) {
+        const int x = s.warp_free[lane];
+        int y = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += up;
+        }
+        s.warp_free[lane] = y - x;
+        if (lane == 31) s.cta_free = y;
+    }
+    cluster.sync();
+    int rank = s.warp_free[warp], free_all = 0;
+    for (int r = 0; r < PG_CLUSTER; ++r) {
+        const int f = *cluster.map_shared_rank(&s.cta_free, r);
+        if (r < cta) rank += f;
+        free_all += f;
+    }
+    cluster.sync();  // no CTA leaves while its count is read; every read of length, and the count of ref, is done
+    const bool fits = free_all >= total;
+    if (cta == 0 && tid == 0 && p.info != nullptr) *p.info = free_all - total;  // negative: pages missing
+    if (!fits) {
+        no_copies();
+        return;
+    }
+
+    // ---- the free pages of ranks below `total` go to their sequences
+    for (int k = s0; k < s1 && rank < total; ++k) {
+        const uint32_t m = free_nibble(p.ref, p.num_pages, k * 32 + lane);
+        const int c = __popc(m);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        int f = rank + incl - c;
+        for (int b = 0; b < 4; ++b) {
+            if (!(m >> b & 1u)) continue;
+            if (f < total) {
+                int lo = 0, hi = p.n - 1;  // the last sequence with start <= f
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (s.start[mid] <= f) lo = mid; else hi = mid - 1;
+                }
+                const int row = p.rows[lo], page = (k * 32 + lane) * 4 + b;
+                if constexpr (FORK) {
+                    const int full = p.length[p.src[lo]] / p.ps;  // a source's length does not change here
+                    p.copy_src[lo] = p.table[(long long)p.src[lo] * p.P + full];
+                    p.copy_dst[lo] = page;
+                    p.table[(long long)row * p.P + full] = page;
+                } else {
+                    // this row's first new entry follows those that its old length holds
+                    const int held = pages_of(p.new_length[lo], p.ps) - (s.start[lo + 1] - s.start[lo]);
+                    p.table[(long long)row * p.P + held + f - s.start[lo]] = page;
+                }
+                p.ref[page] = 1;
+            }
+            ++f;
+        }
+        rank += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if constexpr (!FORK) {
+        for (int i = cta * PG_THREADS + tid; i < p.n; i += PG_CLUSTER * PG_THREADS) p.length[p.rows[i]] = p.new_length[i];
+    } else {
+        // the full pages, shared: a warp a branch
+        for (int i = gw; i < p.n; i += warps) {
+            const int from = p.src[i], row = p.rows[i], len = p.length[from], full = len / p.ps;
+            const int *a = p.table + (long long)from * p.P;
+            int *b = p.table + (long long)row * p.P;
+            for (int j = lane; j < full; j += 32) {
+                const int page = a[j];
+                b[j] = page;
+                if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
+                else report(p.st, DEV_BAD_ARG);
+            }
+            if (lane == 0) {
+                p.length[row] = len;
+                if (len % p.ps == 0) p.copy_src[i] = p.copy_dst[i] = -1;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- compact ----
+// With n live pages, the i-th free page below n (a hole) takes the i-th live
+// page at or above n, both in ascending order: the fewest moves, and no page is
+// both read and written.  Three launches over ref: counts of blocks of pages;
+// ranks of holes and of pages to move; the table, ref and info.  The pools'
+// pages move in pages_copy_kernel.
+constexpr int CP_BLOCK = 4096, CP_THREADS = 1024;
+
+__global__ void __launch_bounds__(CP_THREADS) compact_count_kernel(const PagesParams p) {
+    const int i = blockIdx.x * CP_THREADS + threadIdx.x;
+    const int dead = __popc(free_nibble(p.ref, p.num_pages, i));
+    const int in = min(4, max(0, p.num_pages - 4 * i));
+    __shared__ int sm[33];
+    int total;
+    block_prefix(in - dead, sm, total);
+    if (threadIdx.x == 0) p.ws_counts[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(CP_THREADS) compact_rank_kernel(const PagesParams p, int blocks) {
+    __shared__ int sm[33];
+    const int tid = threadIdx.x;
+    // live pages in all, before this block, and in the blocks before the one that page n lies in
+    int mine = 0, before = 0;
+    for (int b = tid; b < blocks; b += CP_THREADS) {
+        const int c = p.ws_counts[b];
+        mine += c;
+        if (b < (int)blockIdx.x) before += c;
+    }
+    int n, lp0, below;
+    block_prefix(mine, sm, n);
+    block_prefix(before, sm, lp0);
+    const int edge = n / CP_BLOCK;
+    int x = 0;
+    for (int b = tid; b < min(edge, blocks); b += CP_THREADS) x += p.ws_counts[b];
+    for (int q = edge * CP_BLOCK + tid; q < n; q += CP_THREADS) x += p.ref[q] != 0;
+    block_prefix(x, sm, below);  // live pages below n
+    const int i = blockIdx.x * CP_THREADS + tid;
+    const int in = min(4, max(0, p.num_pages - 4 * i));
+    const uint32_t dead = free_nibble(p.ref, p.num_pages, i);
+    int total;
+    int lp = lp0 + block_prefix(in - __popc(dead), sm, total);
+    for (int k = 0; k < in; ++k) {
+        const int q = 4 * i + k;
+        const bool live = !(dead >> k & 1u);
+        if (q < n && !live) p.ws_hole[q - lp] = q;
+        if (q >= n && live) {
+            p.ws_move[lp - below] = q;
+            p.ws_rank[q] = lp - below;
+        }
+        lp += live;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        p.ws_n[0] = n;
+        p.ws_n[1] = n - below;  // pages to move
+        if (p.info != nullptr) *p.info = p.num_pages - n;
+    }
+}
+
+__global__ void __launch_bounds__(256) compact_apply_kernel(const PagesParams p) {
+    const int n = p.ws_n[0], moves = p.ws_n[1];
+    const long long all = (long long)gridDim.x * blockDim.x, me = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    for (long long i = me; i < p.num_pages; i += all) {
+        // below n: a hole's new count comes from the page that moves in; above: a moved page's old count is read first
+        const int v = p.ref[i];
+        if (i < n ? v != 0 : v == 0) p.ref_out[i] = i < n ? v : 0;
+    }
+    for (long long i = me; i < moves; i += all) {
+        const int from = p.ws_move[i], to = p.ws_hole[i];
+        p.ref_out[to] = p.ref[from];
+        p.ref_out[from] = 0;
+    }
+    for (long long i = me; i < (long long)p.R * p.P; i += all) {
+        const int row = (int)(i / p.P), j = (int)(i % p.P);
+        const int page = p.table[i];
+        int to = page;
+        const int len = p.length[row];
+        if (len > 0 && j < pages_of(len, p.ps)) {
+            if (page < 0 || page >= p.num_pages) report(p.st, DEV_BAD_ARG);
+            else if (page >= n) {
+                const int r = p.ws_rank[page];
+                // a page that the table holds but ref does not count has no place to go
+                if (r >= 0 && r < moves && p.ws_move[r] == page) to = p.ws_hole[r];
+                else report(p.st, DEV_BAD_ARG);
+            }
+        }
+        if (to != page || p.table_out != p.table) p.table_out[i] = to;
+    }
+}
+
+// ------------------------------------------------------------------- copy ----
+// pool[o][dst[i]] = pool[o][src[i]] for every pair and outer index, in units of
+// at most 16 KB: 256 threads, four 16-byte loads in flight each, then four
+// stores, and enough blocks on an SM to cover the latency.  A pair whose
+// destination the list names elsewhere too (as a destination or as a source) is
+// not copied: the others read what was there before the call.
+constexpr int COPY_THREADS = 256, COPY_UNIT = 16384;
+
+template <bool CHECK>
+__global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolParams p) {
+    const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
+    const long long per_page = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT, per_pair = per_page * p.outer;
+    const long long units = n * per_pair;
+    const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    int pair = -1, from = 0, to = 0;
+    bool ok = false;
+    for (long long u = u0; u < u1; ++u) {
+        const int i = (int)(u / per_pair);
+        if (i != pair) {
+            pair = i;
+            from = p.src[i];
+            to = p.dst[i];
+            ok = from >= 0 && from < p.num_pages && to >= 0 && to < p.num_pages;
+            bool bad = !ok && !(from == -1 && to == -1);
+            if constexpr (CHECK) {
+                if (ok && from != to) {
+                    bool twice = false;
+                    for (int j = threadIdx.x; j < n; j += COPY_THREADS)
+                        twice |= j != i && (p.dst[j] == to || p.src[j] == to) && !(p.src[j] == -1 && p.dst[j] == -1);
+                    if (__syncthreads_or(twice)) { ok = false; bad = true; }
+                }
+            }
+            if (bad && threadIdx.x == 0) report(p.st, DEV_BAD_ARG);
+        }
+        if (!ok || from == to) continue;
+        const long long in_pair = u % per_pair, o = in_pair / per_page, at = (in_pair % per_page) * COPY_UNIT;
+        const int vecs = (int)(min((long long)COPY_UNIT, p.page_bytes - at) / 16);
+        const uint8_t *base = p.pool + o * p.outer_stride + at;
+        const uint4 *a = reinterpret_cast<const uint4 *>(base + from * p.page_stride);
+        uint4 *b = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(base) + to * p.page_stride);
+        if (vecs == COPY_UNIT / 16) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __ldcs(a + k * COPY_THREADS + threadIdx.x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) __stcs(b + k * COPY_THREADS + threadIdx.x, x[k]);
+        } else {
+            for (int k = threadIdx.x; k < vecs; k += COPY_THREADS) __stcs(b + k, __ldcs(a + k));
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host ----
+cudaError_t launch_pages_free(const PagesParams &p, cudaStream_t stream) {
+    const int grid = (p.n + 7) / 8;
+    pages_free_kernel<<<grid < 296 ? grid : 296, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream) {
+    auto *k = fork ? pages_grant_kernel<true> : pages_grant_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GrantShared));
+    if (e != cudaSuccess) return e;
+    k<<<PG_CLUSTER, PG_THREADS, sizeof(GrantShared), stream>>>(p);
+    return cudaGetLastError();
+}
+int compact_blocks(int num_pages) { return (num_pages + CP_BLOCK - 1) / CP_BLOCK; }
+cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t stream) {
+    const int blocks = compact_blocks(p.num_pages);
+    compact_count_kernel<<<blocks, CP_THREADS, 0, stream>>>(p);
+    compact_rank_kernel<<<blocks, CP_THREADS, 0, stream>>>(p, blocks);
+    const long long want = ((long long)p.R * p.P + 255) / 256, want2 = (p.num_pages + 255) / 256, top = 8LL * sms;
+    const long long grid = want > want2 ? want : want2;
+    compact_apply_kernel<<<(int)(grid < top ? grid : top), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+cudaError_t launch_pages_copy(const PoolParams &p, bool check, int sms, cudaStream_t stream) {
+    const long long units = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT * p.outer * p.n, top = 8LL * sms;
+    const int grid = (int)(units < top ? units : top);
+    if (check) pages_copy_kernel<true><<<grid, COPY_THREADS, 0, stream>>>(p);
+    else pages_copy_kernel<false><<<grid, COPY_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -14,6 +14,11 @@ The entry points mirror ``include/kda.h``:
 * ``workspace_bytes`` / ``release_workspace`` -> ``kda_chunk_fwd_workspace_bytes`` /
   ``kda_release_workspace``
 
+* ``paged_attn`` -> ``kda_paged_attn`` (attention of new tokens over a paged cache: the
+  full-attention layers of a hybrid stack); ``pages_reserve``, ``pages_fork``, ``pages_free``,
+  ``pages_compact``, ``pages_copy`` -> ``kda_pages_*`` (that cache's pages, and pools of
+  recurrent states)
+
 * ``chunk_fwd_host`` -> ``kda_chunk_fwd_host`` (the prefill on host tensors, pinned for
   overlap: the library streams pieces of the token axis up, through the prefill and back)
 
@@ -39,7 +44,9 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_host", "kda
             "kda_status_string", "kda_stream_status", "kda_chunk_fwd_debug_wait_limit",
             "kda_chunk_fwd_debug_inject_timeout", "kda_chunk_fwd_debug_force_exact", "kda_chunk_fwd_debug_block_refs", "kda_chunk_fwd_debug_record_cap", "kda_chunk_fwd_debug_parts",
             "kda_debug_kernel_timing", "kda_debug_kernel_times", "kda_debug_kernel_launches",
-            "kda_abi_version")
+            "kda_paged_attn", "kda_paged_attn_workspace_bytes", "kda_pages_reserve", "kda_pages_fork",
+            "kda_pages_free", "kda_pages_compact", "kda_pages_compact_workspace_bytes", "kda_pages_compact_pool",
+            "kda_pages_copy", "kda_abi_version")
 
 _lib = None          # the library the calls below go through
 _libs = {}           # path -> loaded library
@@ -129,6 +136,21 @@ def _open(path):
     ll = ctypes.POINTER(ctypes.c_longlong)
     lib.kda_debug_kernel_launches.argtypes = [ctypes.POINTER(ctypes.c_int), ll, ll, i, ctypes.POINTER(ctypes.c_int)]
     lib.kda_debug_kernel_launches.restype = i
+    ll, sz = ctypes.c_longlong, ctypes.c_size_t
+    lib.kda_paged_attn.argtypes = [vp] * 9 + [f, vp, vp] + [i] * 10 + [ll] * 3 + [vp, i, vp, sz, vp]
+    lib.kda_paged_attn_workspace_bytes.argtypes = [i] * 8
+    lib.kda_paged_attn_workspace_bytes.restype = sz
+    lib.kda_pages_reserve.argtypes = [vp] * 5 + [i, vp] + [i] * 4 + [vp]
+    lib.kda_pages_fork.argtypes = [vp] * 5 + [i, vp, vp, vp] + [i] * 4 + [vp]
+    lib.kda_pages_free.argtypes = [vp] * 4 + [i] * 5 + [vp]
+    lib.kda_pages_compact.argtypes = [vp] * 6 + [i] * 4 + [vp, sz, vp]
+    lib.kda_pages_compact_workspace_bytes.argtypes = [i]
+    lib.kda_pages_compact_workspace_bytes.restype = sz
+    lib.kda_pages_compact_pool.argtypes = [vp, ll, ll, ll, ll, i, vp, sz, vp]
+    lib.kda_pages_copy.argtypes = [vp, ll, ll, ll, ll, i, vp, vp, i, vp]
+    for name in ("kda_paged_attn", "kda_pages_reserve", "kda_pages_fork", "kda_pages_free", "kda_pages_compact",
+                 "kda_pages_compact_pool", "kda_pages_copy"):
+        getattr(lib, name).restype = i
     lib.kda_abi_version.restype = i
     _libs[path] = lib
     return lib
@@ -490,3 +512,253 @@ def chunk_fwd_host(q, k, v, g, beta, scale, h0=None, *, out, hT=None, stream=Non
 def set_host_piece(tokens: int) -> None:
     """Test hook: pieces of ``tokens`` tokens for ``chunk_fwd_host`` (0 = automatic)."""
     load().kda_chunk_fwd_host_debug_piece(int(tokens))
+
+
+# ------------------------------------------------------------- paged cache ----
+def _on(ref, stream):
+    """Context of the tensors' device and of the stream that the call runs on, so that what
+    the call allocates belongs to that stream; and the stream."""
+    if not ref.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(ref.device)
+    elif stream.device != ref.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {ref.device}")
+    return torch.cuda.stream(stream), stream
+
+
+def _check_on(t, name, dtype, shape, device):
+    _check(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _check_heads(t, name, dtype, shape, device):
+    """A [tokens, heads, d] tensor whose tokens may lie apart (a slice of a fused
+    projection); returns the elements between them."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    n, h, d = shape
+    if n == 0:
+        return h * d
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _pages_strides(t, name, dtype, shape, device):
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    # a stride along one entry says nothing; give it the dense value
+    d = shape[3]
+    st = [t.stride(0), t.stride(1), t.stride(2)]
+    for i, dense in ((2, d), (1, d * shape[2]), (0, d * shape[2] * shape[1])):
+        if shape[i] == 1:
+            st[i] = dense
+        elif st[i] < d:
+            raise ValueError(f"{name}: tokens, heads and pages must not overlap")
+    return st
+
+
+def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k_new=None, v_new=None, rows=None,
+               out=None, lse=None, stream=None):
+    """Attention of a packed batch of new tokens over a paged cache (see ``kda.h``).
+
+    q [total_q,Hq,d] bf16 or fp16, its tokens contiguous or a slice of a wider row; k_pages,
+    v_pages [num_pages,page_size,Hkv,d] of any strides with contiguous channels; cu_q int32
+    [N+1]; page_table int32 [R,P]; length int32 [R], the rows' tokens with the new ones; rows
+    int32 [N] or None (rows 0..N-1); max_q the most new tokens that a sequence has.  k_new,
+    v_new [total_q,Hkv,d] are written to their pages first; without them the cache holds them.
+    Returns out [total_q,Hq,d]; lse fp32 [total_q,Hq] is written when given."""
+    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or cu_q.dim() != 1 or cu_q.numel() < 2:
+        raise ValueError("q must be [total_q,Hq,d], k_pages [num_pages,page_size,Hkv,d], page_table [R,P], cu_q [N+1]")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    ctx, stream = _on(q, stream)
+    dev, dt = q.device, q.dtype
+    total, Hq, d = q.shape
+    num_pages, ps, Hkv, _ = k_pages.shape
+    R, P = page_table.shape
+    N = cu_q.numel() - 1
+    qs = _check_heads(q, "q", dt, (total, Hq, d), dev)
+    strides = _pages_strides(k_pages, "k_pages", dt, (num_pages, ps, Hkv, d), dev)
+    strides += _pages_strides(v_pages, "v_pages", dt, (num_pages, ps, Hkv, d), dev)
+    _check_on(cu_q, "cu_q", torch.int32, (N + 1,), dev)
+    _check_on(page_table, "page_table", torch.int32, (R, P), dev)
+    _check_on(length, "length", torch.int32, (R,), dev)
+    if rows is not None:
+        _check_on(rows, "rows", torch.int32, (N,), dev)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new come together")
+    ks = vs = Hkv * d
+    if k_new is not None:
+        ks = _check_heads(k_new, "k_new", dt, (total, Hkv, d), dev)
+        vs = _check_heads(v_new, "v_new", dt, (total, Hkv, d), dev)
+    if lse is not None:
+        _check_on(lse, "lse", torch.float32, (total, Hq), dev)
+    with ctx:
+        if out is None:
+            out = torch.empty((total, Hq, d), device=dev, dtype=dt)
+        _check_on(out, "out", dt, (total, Hq, d), dev)
+        nbytes = paged_attn_workspace_bytes(N, total, max_q, Hq, Hkv, d, ps, P)
+        ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+        rc = load().kda_paged_attn(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(cu_q),
+                                   _ptr(page_table), _ptr(length), _ptr(rows), float(scale), _ptr(out), _ptr(lse),
+                                   N, total, int(max_q), Hq, Hkv, d, ps, num_pages, P, R, qs, ks, vs,
+                                   (ctypes.c_longlong * 6)(*strides), 0 if dt == torch.bfloat16 else 1,
+                                   _ptr(ws), nbytes, ctypes.c_void_p(stream.cuda_stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_paged_attn")
+    return out
+
+
+def paged_attn_workspace_bytes(N, total_q, max_q, Hq, Hkv, d, page_size, P) -> int:
+    """Device memory that one ``paged_attn`` of these sizes uses while it runs."""
+    return int(load().kda_paged_attn_workspace_bytes(int(N), int(total_q), int(max_q), int(Hq), int(Hkv), int(d),
+                                                     int(page_size), int(P)))
+
+
+def _cache(table, length, ref, dev):
+    if table.dim() != 2 or ref.dim() != 1:
+        raise ValueError("table must be [R,P], ref [num_pages]")
+    R, P = table.shape
+    _check_on(table, "table", torch.int32, (R, P), dev)
+    _check_on(length, "length", torch.int32, (R,), dev)
+    _check_on(ref, "ref", torch.int32, (ref.numel(),), dev)
+    return R, P, ref.numel()
+
+
+def _pool(t, num_pages, dev):
+    """(pointer, outer, outer stride, page stride, page bytes) of a pool [outer, num_pages, ...]
+    whose pages are contiguous."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"a pool must be on {dev}")
+    if t.dim() < 3 or t.shape[1] != num_pages:
+        raise ValueError(f"a pool must be [outer, {num_pages}, ...], got {tuple(t.shape)}")
+    want = 1
+    for k in range(t.dim() - 1, 1, -1):
+        if t.shape[k] != 1 and t.stride(k) != want:
+            raise ValueError("a pool's pages must be contiguous")
+        want *= t.shape[k]
+    es = t.element_size()
+    page = want * es
+    ps = t.stride(1) * es if t.shape[1] > 1 else page
+    os_ = t.stride(0) * es if t.shape[0] > 1 else ps * num_pages
+    return _ptr(t), t.shape[0], os_, ps, page
+
+
+def pages_reserve(table, length, ref, rows, new_length, page_size, *, info=None, stream=None):
+    """Grows rows (int32 [n]) to new_length (int32 [n]), with the lowest-numbered free pages
+    in the list's order; in place.  info int32 [1], when given, receives the free pages left,
+    or minus the number missing, and then nothing has changed."""
+    ctx, stream = _on(table, stream)
+    dev = table.device
+    R, P, num_pages = _cache(table, length, ref, dev)
+    n = rows.numel()
+    _check_on(rows, "rows", torch.int32, (n,), dev)
+    _check_on(new_length, "new_length", torch.int32, (n,), dev)
+    if info is not None:
+        _check_on(info, "info", torch.int32, (1,), dev)
+    with ctx:
+        rc = load().kda_pages_reserve(_ptr(table), _ptr(length), _ptr(ref), _ptr(rows), _ptr(new_length), n, _ptr(info),
+                                      R, P, num_pages, int(page_size), ctypes.c_void_p(stream.cuda_stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_pages_reserve")
+
+
+def pages_fork(table, length, ref, src, dst, page_size, *, pools=(), info=None, stream=None):
+    """Empty rows dst (int32 [n]) share the sequences of rows src: full pages by count, a
+    partial last page copied in every pool [outer, num_pages, ...].  Returns (copy_src,
+    copy_dst), int32 [n], the pages copied (-1, -1: none).  info as ``pages_reserve``."""
+    ctx, stream = _on(table, stream)
+    dev = table.device
+    R, P, num_pages = _cache(table, length, ref, dev)
+    n = src.numel()
+    _check_on(src, "src", torch.int32, (n,), dev)
+    _check_on(dst, "dst", torch.int32, (n,), dev)
+    if info is not None:
+        _check_on(info, "info", torch.int32, (1,), dev)
+    args = [_pool(t, num_pages, dev) for t in pools]
+    with ctx:
+        pairs = torch.empty((2, n), device=dev, dtype=torch.int32)
+        cs, cd = pairs[0], pairs[1]
+        st = ctypes.c_void_p(stream.cuda_stream)
+        rc = load().kda_pages_fork(_ptr(table), _ptr(length), _ptr(ref), _ptr(src), _ptr(dst), n, _ptr(cs), _ptr(cd),
+                                   _ptr(info), R, P, num_pages, int(page_size), st)
+        if rc != KDA_OK:
+            raise KdaError(rc, "kda_pages_fork")
+        for a in args:
+            rc = load().kda_pages_copy(*a, num_pages, _ptr(cs), _ptr(cd), n, st)
+            if rc != KDA_OK:
+                raise KdaError(rc, "kda_pages_copy")
+    return cs, cd
+
+
+def pages_free(table, length, ref, rows, page_size, *, stream=None):
+    """Ends the sequences of rows (int32 [n]), in place."""
+    ctx, stream = _on(table, stream)
+    dev = table.device
+    R, P, num_pages = _cache(table, length, ref, dev)
+    n = rows.numel()
+    _check_on(rows, "rows", torch.int32, (n,), dev)
+    with ctx:
+        rc = load().kda_pages_free(_ptr(table), _ptr(length), _ptr(ref), _ptr(rows), n, R, P, num_pages, int(page_size),
+                                   ctypes.c_void_p(stream.cuda_stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_pages_free")
+
+
+def pages_compact(table, length, ref, page_size, *, table_out=None, ref_out=None, pools=(), info=None, stream=None):
+    """Moves the live pages of every pool [outer, num_pages, ...] to the front and renumbers
+    table and ref, in place or into table_out and ref_out.  Returns (table, ref) as written;
+    info int32 [1], when given, receives the number of free pages."""
+    ctx, stream = _on(table, stream)
+    dev = table.device
+    R, P, num_pages = _cache(table, length, ref, dev)
+    table_out = table if table_out is None else table_out
+    ref_out = ref if ref_out is None else ref_out
+    _check_on(table_out, "table_out", torch.int32, (R, P), dev)
+    _check_on(ref_out, "ref_out", torch.int32, (num_pages,), dev)
+    if info is not None:
+        _check_on(info, "info", torch.int32, (1,), dev)
+    args = [_pool(t, num_pages, dev) for t in pools]
+    with ctx:
+        nbytes = int(load().kda_pages_compact_workspace_bytes(num_pages))
+        ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+        st = ctypes.c_void_p(stream.cuda_stream)
+        rc = load().kda_pages_compact(_ptr(table), _ptr(length), _ptr(ref), _ptr(table_out), _ptr(ref_out), _ptr(info),
+                                      R, P, num_pages, int(page_size), _ptr(ws), nbytes, st)
+        if rc != KDA_OK:
+            raise KdaError(rc, "kda_pages_compact")
+        for a in args:
+            rc = load().kda_pages_compact_pool(*a, num_pages, _ptr(ws), nbytes, st)
+            if rc != KDA_OK:
+                raise KdaError(rc, "kda_pages_compact_pool")
+    return table_out, ref_out
+
+
+def pages_copy(pool, src, dst, *, stream=None):
+    """pool[:, dst[i]] = pool[:, src[i]] for int32 [n] src, dst, on a pool [outer, num_pages, ...]
+    with contiguous pages: key/value pages of every layer, or recurrent states in slots."""
+    ctx, stream = _on(pool, stream)
+    dev = pool.device
+    if pool.dim() < 3:
+        raise ValueError("a pool must be [outer, num_pages, ...]")
+    a = _pool(pool, pool.shape[1], dev)
+    n = src.numel()
+    _check_on(src, "src", torch.int32, (n,), dev)
+    _check_on(dst, "dst", torch.int32, (n,), dev)
+    with ctx:
+        rc = load().kda_pages_copy(*a, pool.shape[1], _ptr(src), _ptr(dst), n, ctypes.c_void_p(stream.cuda_stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_pages_copy")

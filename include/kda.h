@@ -366,11 +366,165 @@ KDA_API int kda_release_workspace(void);
 KDA_API const char *kda_status_string(int status);
 
 /*
+ * The paged cache.
+ *
+ * The models that KDA is for are hybrids: three recurrent layers to one layer
+ * of full attention (section 2 of the Baidu breakdown; "The 3:1 Hybrid
+ * Architecture" of the "Kimi Linear" explainer).  A server of one keeps, next
+ * to the recurrent states, the full-attention layers' keys and values in pages,
+ * and reuses both across requests.  A cache is
+ *
+ *   table  : int32 [R, P]        page numbers; row r is a sequence's slot, its
+ *                                first ceil(length[r] / page_size) entries are
+ *                                in use and the others -1
+ *   length : int32 [R]           tokens in each row
+ *   ref    : int32 [num_pages]   rows that hold each page (0: free)
+ *
+ * all in DEVICE memory, never read by the host, with one or more pools of
+ * num_pages pages: key and value pages, or the recurrent states themselves (a
+ * state [H, dk, dv] in a slot is a page of a pool too).  Calls on one cache
+ * must be ordered by the caller (one stream, or events).  What is found bad on
+ * the device (a page or row number out of range, a list that names a row
+ * twice, a length that does not fit) makes no kernel read or write outside the
+ * buffers and is reported by kda_stream_status() as KDA_ERR_INVALID_ARG.
+ */
+
+/* 16-bit types of kda_paged_attn. */
+enum { KDA_BF16 = 0, KDA_FP16 = 1 };
+
+/*
+ * kda_paged_attn -- softmax attention of new tokens over a paged cache: single
+ * tokens (decode), a few drafted tokens, chunks of a prompt, or all of them in
+ * one packed batch.  The new tokens' keys and values are written to their
+ * pages by the same call.
+ *
+ *   q          : [total_q, Hq, d]   new tokens of the N sequences back to back
+ *   k_new      : [total_q, Hkv, d]  their keys and values, or both NULL when
+ *   v_new      : [total_q, Hkv, d]  the cache holds them already
+ *   k_pages    : [num_pages, page_size, Hkv, d], or as page_strides says
+ *   v_pages    : likewise
+ *   cu_q       : int32 [N + 1]  sequence n's new tokens are cu_q[n] .. cu_q[n+1] - 1;
+ *                starts at 0, never decreases, ends at total_q or before it
+ *                (rows of out and lse behind the last sequence are left as they were)
+ *   page_table : int32 [R, P]   see above
+ *   length     : int32 [R]      tokens of a row WITH the new ones
+ *   rows       : int32 [N] the sequences' rows of page_table and length, or
+ *                NULL for rows 0 .. N - 1
+ *   scale      : > 0, finite (commonly d^-0.5)
+ *   out        : [total_q, Hq, d]
+ *   lse        : fp32 [total_q, Hq] log of the sum of exp(scale q.k), or NULL
+ *   max_q      : no sequence has more new tokens than this
+ *   q_stride, k_stride, v_stride : elements between tokens of q, k_new, v_new
+ *                (heads and channels are dense)
+ *   page_strides : HOST array of 6, elements between pages, tokens and heads of
+ *                k_pages, then of v_pages; NULL for the dense layout above
+ *   dtype      : KDA_BF16 or KDA_FP16, of q, k, v and out
+ *   workspace  : kda_paged_attn_workspace_bytes() bytes, 16-byte aligned, of
+ *                the caller; a call's alone until it is done, contents of no
+ *                consequence before and after
+ *
+ * Token i of sequence n, of n_q new ones, is at position p = length - n_q + i.
+ * It attends keys 0 .. p: o = sum_j softmax_j(scale q.k_j) v_j, query head h
+ * reading key head h / (Hq / Hkv).  A position below 0 has no place and no
+ * key: nothing is written for it, its out is 0 and its lse -inf.  Products
+ * take 16-bit operands (the softmax weights are rounded to dtype, their sum is
+ * not) and accumulate in fp32.  Keys and values of positions below length must
+ * be finite; whatever pages hold behind them, NaN included, has no effect.
+ * Positions that are written must lie in pages of one row of the call only.
+ * Nothing is allocated, so calls can be captured into graphs; lengths, rows and
+ * pages may change between replays, sizes may not.
+ *
+ * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; N >= 1; pointers
+ * to 16-bit data 16-byte aligned and their strides multiples of 8 elements;
+ * P * page_size and total_q * Hq below 2^31 - 4096.  total_q == 0 does nothing.
+ */
+KDA_API int kda_paged_attn(const void *q, const void *k_new, const void *v_new,
+                  void *k_pages, void *v_pages, const int *cu_q,
+                  const int *page_table, const int *length, const int *rows,
+                  float scale, void *out, float *lse,
+                  int N, int total_q, int max_q, int Hq, int Hkv, int d,
+                  int page_size, int num_pages, int P, int R,
+                  long long q_stride, long long k_stride, long long v_stride,
+                  const long long *page_strides, int dtype,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_paged_attn for these sizes on the current device (0 when
+ * they are unsupported or total_q == 0). */
+KDA_API size_t kda_paged_attn_workspace_bytes(int N, int total_q, int max_q, int Hq, int Hkv, int d,
+                  int page_size, int P);
+
+/*
+ * kda_pages_reserve -- pages for rows to grow into.  Row rows[i] gets
+ * length new_length[i] (>= its length so far) and the pages that this needs,
+ * the lowest-numbered free ones, in the order of the list; their ref becomes 1.
+ * All or nothing: with too few free pages, or a bad list, nothing changes.
+ *
+ *   rows, new_length : int32 [n], n <= 8192, every row once
+ *   info             : int32 [1] or NULL: free pages left, or minus the number
+ *                      of pages missing (not written for a bad list)
+ *
+ * Sizes: R <= 65536, R * P and P * page_size below 2^31, num_pages <= 2^30.
+ */
+KDA_API int kda_pages_reserve(int *table, int *length, int *ref, const int *rows, const int *new_length,
+                  int n, int *info, int R, int P, int num_pages, int page_size, void *stream);
+
+/*
+ * kda_pages_fork -- row dst_rows[i] becomes a second holder of row
+ * src_rows[i]'s sequence: it shares the full pages (their ref grows), and a
+ * partial last page is copied to the lowest-numbered free page, so that both
+ * rows can go on writing.  copy_src[i], copy_dst[i] (int32 [n]) receive that
+ * copy, for kda_pages_copy on every pool, or -1, -1 where there is none.  A
+ * source may be named often; a destination must be empty (length 0) and be
+ * named once.  All or nothing, info and sizes as kda_pages_reserve; when
+ * nothing changes every copy is -1, -1.
+ */
+KDA_API int kda_pages_fork(int *table, int *length, int *ref, const int *src_rows, const int *dst_rows, int n,
+                  int *copy_src, int *copy_dst, int *info, int R, int P, int num_pages, int page_size,
+                  void *stream);
+
+/*
+ * kda_pages_free -- rows[0 .. n) end: each of their pages loses a holder (and is
+ * free at 0), their entries become -1, their length 0.  A list that names a row
+ * twice or out of range changes nothing.  Sizes as kda_pages_reserve, any n <= R.
+ */
+KDA_API int kda_pages_free(int *table, int *length, int *ref, const int *rows, int n,
+                  int R, int P, int num_pages, int page_size, void *stream);
+
+/*
+ * kda_pages_compact -- live pages moved to the front: with n of them, the i-th
+ * free page below n takes the i-th live page at or above n.  Writes the
+ * renumbered table and ref (table_out, ref_out may be table and ref
+ * themselves) and info[0] = free pages (info may be NULL).  The moves stay in
+ * the workspace (kda_pages_compact_workspace_bytes(num_pages) bytes, 16-byte
+ * aligned) for kda_pages_compact_pool, to be called on every pool next: the
+ * pages' contents have not moved before that.
+ */
+KDA_API int kda_pages_compact(const int *table, const int *length, const int *ref, int *table_out, int *ref_out,
+                  int *info, int R, int P, int num_pages, int page_size,
+                  void *workspace, size_t workspace_bytes, void *stream);
+KDA_API size_t kda_pages_compact_workspace_bytes(int num_pages);
+KDA_API int kda_pages_compact_pool(void *pool, long long outer, long long outer_stride, long long page_stride,
+                  long long page_bytes, int num_pages, const void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/*
+ * kda_pages_copy -- pages of a pool copied onto others: for every o < outer
+ * (layers, keys and values) and i < n, the page_bytes bytes at pool + o *
+ * outer_stride + src[i] * page_stride go to the same place of page dst[i].
+ * src, dst: int32 [n].  A pair -1, -1 is skipped.  A destination must not be
+ * named a second time, as a destination or as a source: such a pair is left
+ * out and reported.  pool, page_bytes and the strides (in bytes): multiples of
+ * 16; pages do not overlap.
+ */
+KDA_API int kda_pages_copy(void *pool, long long outer, long long outer_stride, long long page_stride,
+                  long long page_bytes, int num_pages, const int *src, const int *dst, int n, void *stream);
+
+/*
  * kda_stream_status -- synchronise `stream`, then read and clear the current
  * device's status word.  Returns KDA_OK, KDA_ERR_TIMEOUT when a kernel's
  * bounded wait gave up since the last call (that kernel's outputs are then
  * unspecified), KDA_ERR_INVALID_ARG when kda_chunk_fwd_varlen found bad
- * offsets, KDA_ERR_BOUNDS when (debug build only) an index check failed, or
+ * offsets or a call on a paged cache a bad list or number, KDA_ERR_BOUNDS when (debug build only) an index check failed, or
  * KDA_ERR_CUDA when the synchronisation itself failed.
  *
  * Debug build.  libkda_debug.so is this library compiled with KDA_DEBUG: the
