@@ -13,7 +13,13 @@ int paged_rows_slots(int ctas);
 int paged_rows_ctas_per_sm(int d);
 int paged_rows_tile();
 cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, int ctas, cudaStream_t stream);
-cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, int entries, int tile_rows, cudaStream_t stream);
+cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, const int *count, int max_entries, int tile_rows, int sms,
+                              cudaStream_t stream);
+int paged_chunk_tile();
+bool paged_chunk_pages(int page_size);
+ChunkLimits paged_chunk_limits(int N, int total_q, int G, int Hkv, int span, int sms);
+size_t paged_chunk_piece_bytes();
+cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void *ws, int d, bool bf, int sms, cudaStream_t stream);
 cudaError_t launch_pages_free(const PagesParams &p, cudaStream_t stream);
 cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream);
 int compact_blocks(int num_pages);
@@ -42,27 +48,44 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
     return KDA_OK;
 }
 
+// Rows of one sequence and key head (new tokens times query heads) up to which the kernel of
+// few rows runs.
+constexpr int kFewRows = 16;
+
 struct AttnPlan {
-    int ctas, entries, slots, tile;
-    size_t off_ml, off_o, bytes;
+    bool chunk;
+    int ctas, entries, tile, sms;
+    kda::ChunkLimits lim;
+    size_t off_entries, off_ml, off_o, bytes;
 };
 AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_size, int P) {
     AttnPlan a = {};
     const int G = Hq / Hkv;
     if (max_q > total_q) max_q = total_q;
-    a.tile = kda::paged_rows_tile();
-    // units that there can be: every sequence's tiles, each over a full table
-    const long long seqs = N < total_q ? N : total_q;
-    const long long tiles = (long long)total_q * G / a.tile + seqs;
-    const long long span = ((long long)P * page_size + 63) / 64;
-    const long long top = (long long)kda::host_num_sms(device()) * kda::paged_rows_ctas_per_sm(d);
-    a.ctas = (int)top;
-    if (tiles < top && tiles * Hkv < top && tiles * Hkv * span < top) a.ctas = (int)(tiles * Hkv * span);
-    a.entries = a.ctas;
-    a.slots = kda::paged_rows_slots(a.ctas);
-    a.off_ml = up256((size_t)a.entries * sizeof(kda::SplitEntry));
-    a.off_o = a.off_ml + up256((size_t)a.slots * a.tile * sizeof(float2));
-    a.bytes = a.off_o + (size_t)a.slots * a.tile * d * sizeof(float);
+    a.sms = kda::host_num_sms(device());
+    a.chunk = (long long)max_q * G > kFewRows && kda::paged_chunk_pages(page_size);
+    long long rows;
+    if (a.chunk) {
+        a.tile = kda::paged_chunk_tile();
+        a.lim = kda::paged_chunk_limits(N, total_q, G, Hkv, P * page_size, a.sms);
+        a.entries = a.lim.entries;
+        a.off_entries = 256 + up256((size_t)N * sizeof(int)) + up256((size_t)a.lim.pieces * kda::paged_chunk_piece_bytes());
+        rows = a.lim.rows;
+    } else {
+        a.tile = kda::paged_rows_tile();
+        // units that there can be: every sequence's tiles, each over a full table
+        const long long seqs = N < total_q ? N : total_q;
+        const long long tiles = (long long)total_q * G / a.tile + seqs;
+        const long long span = ((long long)P * page_size + 63) / 64;
+        const long long top = (long long)a.sms * kda::paged_rows_ctas_per_sm(d);
+        a.ctas = (int)top;
+        if (tiles < top && tiles * Hkv < top && tiles * Hkv * span < top) a.ctas = (int)(tiles * Hkv * span);
+        a.entries = a.ctas;
+        rows = (long long)kda::paged_rows_slots(a.ctas) * a.tile;
+    }
+    a.off_ml = a.off_entries + up256((size_t)a.entries * sizeof(kda::SplitEntry));
+    a.off_o = a.off_ml + up256((size_t)rows * sizeof(float2));
+    a.bytes = a.off_o + (size_t)rows * d * sizeof(float);
     return a;
 }
 
@@ -162,7 +185,7 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
     const long long *ps = page_strides ? page_strides : dense;
     if (q_stride < (long long)Hq * d || (k_new && (k_stride < row || v_stride < row))) return KDA_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i) {
-        if (ps[i] < 0 || ps[i] > (1LL << 38)) return KDA_ERR_INVALID_ARG;
+        if (ps[i] < d || ps[i] > (1LL << 38)) return KDA_ERR_INVALID_ARG;  // tokens, heads and pages do not overlap
         if (ps[i] % 8) return KDA_ERR_ALIGNMENT;
     }
     if (q_stride % 8 || (k_new && (k_stride % 8 || v_stride % 8)) || !al(q, 16) || !al(k_new, 16) || !al(v_new, 16) ||
@@ -206,12 +229,19 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
     p.v_ts = ps[4];
     p.v_hs = ps[5];
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.entries = reinterpret_cast<kda::SplitEntry *>(ws);
+    p.entries = reinterpret_cast<kda::SplitEntry *>(ws + pl.off_entries);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (kda::launch_paged_rows(p, d, dtype == KDA_BF16, pl.ctas, s) != cudaSuccess) return KDA_ERR_CUDA;
-    return to_status(kda::launch_paged_join(p, d, dtype == KDA_BF16, pl.entries, pl.tile, s));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = dtype == KDA_BF16;
+    if (pl.chunk) {
+        if (kda::launch_paged_chunk(p, pl.lim, ws, d, bf, pl.sms, s) != cudaSuccess) return KDA_ERR_CUDA;
+        if (pl.lim.rows == 0) return KDA_OK;  // nothing can be split
+        const int *count = reinterpret_cast<const int *>(ws) + 2;  // ChunkPlanHead::entries
+        return to_status(kda::launch_paged_join(p, d, bf, count, pl.entries, pl.tile, pl.sms, s));
+    }
+    if (kda::launch_paged_rows(p, d, bf, pl.ctas, s) != cudaSuccess) return KDA_ERR_CUDA;
+    return to_status(kda::launch_paged_join(p, d, bf, nullptr, pl.entries, pl.tile, pl.sms, s));
 }
 
 int kda_pages_reserve(int *table, int *length, int *ref, const int *rows, const int *new_length, int n, int *info, int R,

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
             // runs c + 1 .. last hold the rest: the last is the one with the item's last unit
             const long long e = start + units;
             const int last = (int)((e * runs + W - 1) / W) - 1;
-            p.entries[c] = {n, h, t, grid + c, c + 1, last - c};
+            p.entries[c] = {n, h, t, (grid + c) * PA_ROWS, (c + 1) * PA_ROWS, last - c, PA_ROWS};
         }
         __syncthreads();
 
@@ -383,46 +383,52 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
     }
 }
 
-// Joins the pieces of a split item: entry blockIdx.x, four rows per block, one
-// warp per row.  Reads each piece's row once; with the pieces of a run of CTAs
-// still in L2 it is bound by latency, so a lane keeps four loads in flight.
+// Joins the pieces of split items, one warp per row: entries in turn over
+// blockIdx.x, rows over blockIdx.y.  The pieces have just been written and lie
+// in L2, so a lane keeps four loads in flight and that is enough.
 template <int D, bool BF>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p, int tile_rows) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int tile_rows, const int *count, int max_entries) {
     wait_for_primary();
-    const SplitEntry e = p.entries[blockIdx.x];
-    if (e.count == 0) return;
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const PagedSeq s = paged_seq(p, e.n, false);
-    const int row = e.t * tile_rows + r;
-    if (r >= tile_rows || row >= s.nq * p.G) return;
-    auto slot = [&](int i) { return (long long)(i == 0 ? e.head : e.next + i - 1) * tile_rows + r; };
-    float M = -INFINITY;
-    for (int i = lane; i <= e.count; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+    const int entries = count != nullptr ? min(*count, max_entries) : max_entries;
+    const int lane = threadIdx.x & 31, warps = gridDim.y * (blockDim.x >> 5);
+    for (int i = blockIdx.x; i < entries; i += gridDim.x) {
+        const SplitEntry e = p.entries[i];
+        if (e.count == 0) continue;
+        const PagedSeq s = paged_seq(p, e.n, false);
+        const int rows = min(tile_rows, s.nq * p.G - e.t * tile_rows);
+        for (int r = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
+            auto at = [&](int k) { return (long long)(k == 0 ? e.head : e.next + (k - 1) * e.stride) + r; };
+            float M = -INFINITY;
+            for (int k = lane; k <= e.count; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == -INFINITY ? 0.f : M;
-    constexpr int V = D / 32;
-    float a[V] = {}, L = 0.f;
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float ref = M == -INFINITY ? 0.f : M;
+            constexpr int V = D / 32;
+            float a[V] = {}, L = 0.f;
 #pragma unroll 4
-    for (int i = 0; i <= e.count; ++i) {
-        const float2 ml = p.part_ml[slot(i)];
-        const float f = ex2(ml.x - ref);
-        L += f * ml.y;
-        const float *src = p.part_o + slot(i) * D + lane * V;
+            for (int k = 0; k <= e.count; ++k) {
+                const float2 ml = p.part_ml[at(k)];
+                const float f = ex2(ml.x - ref);
+                L += f * ml.y;
+                const float *src = p.part_o + at(k) * D + lane * V;
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const float2 y = *reinterpret_cast<const float2 *>(src + j);
-            a[j] += f * y.x;
-            a[j + 1] += f * y.y;
+                for (int j = 0; j < V; j += 2) {
+                    const float2 y = *reinterpret_cast<const float2 *>(src + j);
+                    a[j] += f * y.x;
+                    a[j + 1] += f * y.y;
+                }
+            }
+            const float inv = M == -INFINITY ? 0.f : 1.f / L;
+            const int row = e.t * tile_rows + r, head = e.h * p.G + row % p.G;
+            const long long tok = s.q0 + row / p.G;
+#pragma unroll
+            for (int j = 0; j < V; j += 2)
+                *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + head) * D + lane * V + j) =
+                    pack16x2<BF>(a[j] * inv, a[j + 1] * inv);
+            if (p.lse != nullptr && lane == 0)
+                p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
         }
     }
-    const float inv = M == -INFINITY ? 0.f : 1.f / L;
-    const long long tok = s.q0 + row / p.G;
-    const int head = e.h * p.G + row % p.G;
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-        *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + head) * D + lane * V + j) = pack16x2<BF>(a[j] * inv, a[j + 1] * inv);
-    if (p.lse != nullptr && lane == 0) p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
 }
 
 // ------------------------------------------------------------------- host ----
@@ -438,27 +444,32 @@ static cudaError_t launch_rows_t(const PagedParams &p, int ctas, cudaStream_t st
     return cudaGetLastError();
 }
 template <int D, bool BF>
-static cudaError_t launch_join_t(const PagedParams &p, int entries, int tile_rows, cudaStream_t stream) {
+static cudaError_t launch_join_t(const PagedParams &p, const int *count, int max_entries, int tile_rows, int sms, cudaStream_t stream) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(entries, (tile_rows + 3) / 4);
-    cfg.blockDim = dim3(128);
+    const int groups = tile_rows > 64 ? 8 : 2;  // blocks of eight warps over an item's rows
+    cfg.gridDim = dim3(max_entries < 2 * sms ? max_entries : 2 * sms, groups);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF>, p, tile_rows);
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF>, p, tile_rows, count, max_entries);
 }
 
 cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, int ctas, cudaStream_t stream) {
     if (d == 128) return bf ? launch_rows_t<128, true>(p, ctas, stream) : launch_rows_t<128, false>(p, ctas, stream);
     return bf ? launch_rows_t<64, true>(p, ctas, stream) : launch_rows_t<64, false>(p, ctas, stream);
 }
-cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, int entries, int tile_rows, cudaStream_t stream) {
+// count: entries, on the device, or NULL for max_entries of them (some with count 0).
+cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, const int *count, int max_entries, int tile_rows, int sms,
+                              cudaStream_t stream) {
     if (d == 128)
-        return bf ? launch_join_t<128, true>(p, entries, tile_rows, stream) : launch_join_t<128, false>(p, entries, tile_rows, stream);
-    return bf ? launch_join_t<64, true>(p, entries, tile_rows, stream) : launch_join_t<64, false>(p, entries, tile_rows, stream);
+        return bf ? launch_join_t<128, true>(p, count, max_entries, tile_rows, sms, stream)
+                  : launch_join_t<128, false>(p, count, max_entries, tile_rows, sms, stream);
+    return bf ? launch_join_t<64, true>(p, count, max_entries, tile_rows, sms, stream)
+              : launch_join_t<64, false>(p, count, max_entries, tile_rows, sms, stream);
 }
 
 }  // namespace kda

@@ -9,12 +9,19 @@
 
 namespace kda {
 
-// One row's partial result over part of its keys: unnormalised sums against
-// the running maximum m (log2 units), l = sum of 2^(x - m).  The pieces of a
-// split item lie in slots of `rows` rows: `head`, then next .. next + count - 1.
+// One row's partial result over part of its keys: unnormalised sums against a
+// reference m (log2 units) and l = sum of 2^(x - m).  The first piece of a split
+// item has its rows from part row `head`, the `count` others from `next`,
+// `stride` rows apart.
 struct SplitEntry {
     int n, h, t;     // sequence, key head, row tile
-    int head, next, count;  // count = 0: nothing to join
+    int head, next, count, stride;  // count = 0: nothing to join
+};
+
+// Upper bounds of the chunk kernel's plan: pieces of work, split items, rows of
+// partial sums.
+struct ChunkLimits {
+    int pieces, entries, rows;
 };
 
 struct PagedParams {
@@ -28,8 +35,8 @@ struct PagedParams {
     long long q_ts, kn_ts, vn_ts;       // elements between tokens
     long long k_ps, k_ts, k_hs;         // key pages: elements between pages, tokens, heads
     long long v_ps, v_ts, v_hs;         // value pages
-    float *part_o;                      // [slots][rows][d]
-    float2 *part_ml;                    // [slots][rows]
+    float *part_o;                      // [part rows][d]
+    float2 *part_ml;                    // [part rows]
     SplitEntry *entries;
     DeviceStatus st;
 };

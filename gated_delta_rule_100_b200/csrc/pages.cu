@@ -126,8 +126,7 @@ __device__ __forceinline__ uint32_t free_nibble(const int *ref, int num_pages, i
 
 template <bool FORK>
 __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS) pages_grant_kernel(const PagesParams p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    GrantShared &s = *reinterpret_cast<GrantShared *>(raw);
+    __shared__ GrantShared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -417,10 +416,8 @@ cudaError_t launch_pages_free(const PagesParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream) {
-    auto *k = fork ? pages_grant_kernel<true> : pages_grant_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GrantShared));
-    if (e != cudaSuccess) return e;
-    k<<<PG_CLUSTER, PG_THREADS, sizeof(GrantShared), stream>>>(p);
+    if (fork) pages_grant_kernel<true><<<PG_CLUSTER, PG_THREADS, 0, stream>>>(p);
+    else pages_grant_kernel<false><<<PG_CLUSTER, PG_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 int compact_blocks(int num_pages) { return (num_pages + CP_BLOCK - 1) / CP_BLOCK; }

@@ -515,59 +515,76 @@ def set_host_piece(tokens: int) -> None:
 
 
 # ------------------------------------------------------------- paged cache ----
-def _on(ref, stream):
-    """Context of the tensors' device and of the stream that the call runs on, so that what
-    the call allocates belongs to that stream; and the stream."""
-    if not ref.is_cuda:
+# A serving step makes many of these calls on little data, so what a call costs on the host
+# counts: the checks compare whole shapes, and device and stream are only switched when they
+# are not the current ones.
+def _here(t, stream):
+    """Whether the call runs on the current device and stream."""
+    if not t.is_cuda:
         raise ValueError("the tensors must be CUDA tensors")
+    return stream is None and torch._C._cuda_getDevice() == t.get_device()
+
+
+def _there(t, stream):
+    """Context of the tensor's device and of the stream that the call runs on, so that what
+    the call allocates belongs to that stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(ref.device)
-    elif stream.device != ref.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {ref.device}")
-    return torch.cuda.stream(stream), stream
+        stream = torch.cuda.current_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
-def _check_on(t, name, dtype, shape, device):
-    _check(t, name, dtype, shape)
+def _raw_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _arr(t, name, dtype, shape, device):
+    """The address of a contiguous tensor that is what the call needs."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _like(t, name, dtype, shape, device):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _check_heads(t, name, dtype, shape, device):
-    """A [tokens, heads, d] tensor whose tokens may lie apart (a slice of a fused
-    projection); returns the elements between them."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _token_stride(t, name, dtype, shape, device):
+    """Elements between the tokens of a [tokens, heads, d] tensor, which may lie apart (a slice
+    of a fused projection)."""
+    _like(t, name, dtype, shape, device)
     n, h, d = shape
-    if n == 0:
-        return h * d
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    st = t.stride()
+    if n and (st[2] != 1 or (h > 1 and st[1] != d)):
         raise ValueError(f"{name}: heads and channels must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return st[0] if n > 1 else h * d
 
 
-def _pages_strides(t, name, dtype, shape, device):
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: channels must be contiguous")
+def _page_strides(t, name, dtype, shape, device):
+    """Elements between the pages, tokens and heads of a pool of pages."""
+    _like(t, name, dtype, shape, device)
+    sp, st, sh, sd = t.stride()
+    n, ps, h, d = shape
     # a stride along one entry says nothing; give it the dense value
-    d = shape[3]
-    st = [t.stride(0), t.stride(1), t.stride(2)]
-    for i, dense in ((2, d), (1, d * shape[2]), (0, d * shape[2] * shape[1])):
-        if shape[i] == 1:
-            st[i] = dense
-        elif st[i] < d:
-            raise ValueError(f"{name}: tokens, heads and pages must not overlap")
-    return st
+    sh, st, sp = (sh if h > 1 else d), (st if ps > 1 else h * d), (sp if n > 1 else ps * h * d)
+    if sd != 1 or sh < d or st < d or sp < d:
+        raise ValueError(f"{name}: channels must be contiguous, and tokens, heads and pages not overlap")
+    return sp, st, sh
+
+
+_attn_bytes = {}
+
+
+def paged_attn_workspace_bytes(N, total_q, max_q, Hq, Hkv, d, page_size, P) -> int:
+    """Device memory that one ``paged_attn`` of these sizes uses while it runs."""
+    return int(load().kda_paged_attn_workspace_bytes(N, total_q, max_q, Hq, Hkv, d, page_size, P))
 
 
 def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k_new=None, v_new=None, rows=None,
@@ -580,98 +597,99 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
     int32 [N] or None (rows 0..N-1); max_q the most new tokens that a sequence has.  k_new,
     v_new [total_q,Hkv,d] are written to their pages first; without them the cache holds them.
     Returns out [total_q,Hq,d]; lse fp32 [total_q,Hq] is written when given."""
+    dt = q.dtype
     if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or cu_q.dim() != 1 or cu_q.numel() < 2:
         raise ValueError("q must be [total_q,Hq,d], k_pages [num_pages,page_size,Hkv,d], page_table [R,P], cu_q [N+1]")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-    ctx, stream = _on(q, stream)
-    dev, dt = q.device, q.dtype
-    total, Hq, d = q.shape
-    num_pages, ps, Hkv, _ = k_pages.shape
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError(f"q must be bfloat16 or float16, got {dt}")
+    if not _here(q, stream):
+        with _there(q, stream):
+            return paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, max_q=max_q, k_new=k_new, v_new=v_new,
+                              rows=rows, out=out, lse=lse)
+    dev, shape = q.device, q.shape
+    total, Hq, d = shape
+    pages = k_pages.shape
+    num_pages, ps, Hkv, _ = pages
     R, P = page_table.shape
     N = cu_q.numel() - 1
-    qs = _check_heads(q, "q", dt, (total, Hq, d), dev)
-    strides = _pages_strides(k_pages, "k_pages", dt, (num_pages, ps, Hkv, d), dev)
-    strides += _pages_strides(v_pages, "v_pages", dt, (num_pages, ps, Hkv, d), dev)
-    _check_on(cu_q, "cu_q", torch.int32, (N + 1,), dev)
-    _check_on(page_table, "page_table", torch.int32, (R, P), dev)
-    _check_on(length, "length", torch.int32, (R,), dev)
-    if rows is not None:
-        _check_on(rows, "rows", torch.int32, (N,), dev)
+    i32 = torch.int32
+    qs = _token_stride(q, "q", dt, shape, dev)
+    strides = _page_strides(k_pages, "k_pages", dt, (num_pages, ps, Hkv, d), dev) \
+        + _page_strides(v_pages, "v_pages", dt, (num_pages, ps, Hkv, d), dev)
+    cu = _arr(cu_q, "cu_q", i32, (N + 1,), dev)
+    tab = _arr(page_table, "page_table", i32, (R, P), dev)
+    ln = _arr(length, "length", i32, (R,), dev)
+    rw = None if rows is None else _arr(rows, "rows", i32, (N,), dev)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new come together")
+    kp = vp = None
     ks = vs = Hkv * d
     if k_new is not None:
-        ks = _check_heads(k_new, "k_new", dt, (total, Hkv, d), dev)
-        vs = _check_heads(v_new, "v_new", dt, (total, Hkv, d), dev)
-    if lse is not None:
-        _check_on(lse, "lse", torch.float32, (total, Hq), dev)
-    with ctx:
-        if out is None:
-            out = torch.empty((total, Hq, d), device=dev, dtype=dt)
-        _check_on(out, "out", dt, (total, Hq, d), dev)
-        nbytes = paged_attn_workspace_bytes(N, total, max_q, Hq, Hkv, d, ps, P)
-        ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
-        rc = load().kda_paged_attn(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(cu_q),
-                                   _ptr(page_table), _ptr(length), _ptr(rows), float(scale), _ptr(out), _ptr(lse),
-                                   N, total, int(max_q), Hq, Hkv, d, ps, num_pages, P, R, qs, ks, vs,
-                                   (ctypes.c_longlong * 6)(*strides), 0 if dt == torch.bfloat16 else 1,
-                                   _ptr(ws), nbytes, ctypes.c_void_p(stream.cuda_stream))
+        new = (total, Hkv, d)
+        ks, vs = _token_stride(k_new, "k_new", dt, new, dev), _token_stride(v_new, "v_new", dt, new, dev)
+        kp, vp = k_new.data_ptr(), v_new.data_ptr()
+    ls = None if lse is None else _arr(lse, "lse", torch.float32, (total, Hq), dev)
+    if out is None:
+        out = torch.empty(shape, device=dev, dtype=dt)
+    op = _arr(out, "out", dt, shape, dev)
+    lib = load()
+    key = (dev, N, total, max_q, Hq, Hkv, d, ps, P)
+    nbytes = _attn_bytes.get(key)
+    if nbytes is None:  # a plan of sizes, the same for every call of them
+        if len(_attn_bytes) > 4096:
+            _attn_bytes.clear()
+        nbytes = _attn_bytes[key] = paged_attn_workspace_bytes(*key[1:])
+    ws = torch.empty(nbytes or 1, device=dev, dtype=torch.uint8)
+    rc = lib.kda_paged_attn(q.data_ptr(), kp, vp, k_pages.data_ptr(), v_pages.data_ptr(), cu, tab, ln, rw, scale, op, ls,
+                            N, total, max_q, Hq, Hkv, d, ps, num_pages, P, R, qs, ks, vs, (ctypes.c_longlong * 6)(*strides),
+                            0 if dt is torch.bfloat16 else 1, ws.data_ptr(), nbytes, _raw_stream(q))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_paged_attn")
     return out
 
 
-def paged_attn_workspace_bytes(N, total_q, max_q, Hq, Hkv, d, page_size, P) -> int:
-    """Device memory that one ``paged_attn`` of these sizes uses while it runs."""
-    return int(load().kda_paged_attn_workspace_bytes(int(N), int(total_q), int(max_q), int(Hq), int(Hkv), int(d),
-                                                     int(page_size), int(P)))
-
-
-def _cache(table, length, ref, dev):
+def _cache(table, length, ref, info, dev):
+    """Addresses and sizes of a cache's table, length and ref, and of info (or None)."""
     if table.dim() != 2 or ref.dim() != 1:
         raise ValueError("table must be [R,P], ref [num_pages]")
-    R, P = table.shape
-    _check_on(table, "table", torch.int32, (R, P), dev)
-    _check_on(length, "length", torch.int32, (R,), dev)
-    _check_on(ref, "ref", torch.int32, (ref.numel(),), dev)
-    return R, P, ref.numel()
+    i32 = torch.int32
+    R, P = shape = table.shape
+    n = ref.numel()
+    return (_arr(table, "table", i32, shape, dev), _arr(length, "length", i32, (R,), dev), _arr(ref, "ref", i32, (n,), dev),
+            None if info is None else _arr(info, "info", i32, (1,), dev), R, P, n)
 
 
 def _pool(t, num_pages, dev):
     """(pointer, outer, outer stride, page stride, page bytes) of a pool [outer, num_pages, ...]
-    whose pages are contiguous."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"a pool must be on {dev}")
-    if t.dim() < 3 or t.shape[1] != num_pages:
-        raise ValueError(f"a pool must be [outer, {num_pages}, ...], got {tuple(t.shape)}")
+    whose pages are contiguous; strides in bytes."""
+    if t.device != dev:
+        raise ValueError(f"a pool must be on {dev}, got {t.device}")
+    shape, st = t.shape, t.stride()
+    if len(shape) < 3 or shape[1] != num_pages:
+        raise ValueError(f"a pool must be [outer, {num_pages}, ...], got {tuple(shape)}")
     want = 1
-    for k in range(t.dim() - 1, 1, -1):
-        if t.shape[k] != 1 and t.stride(k) != want:
+    for k in range(len(shape) - 1, 1, -1):
+        if shape[k] != 1 and st[k] != want:
             raise ValueError("a pool's pages must be contiguous")
-        want *= t.shape[k]
+        want *= shape[k]
     es = t.element_size()
     page = want * es
-    ps = t.stride(1) * es if t.shape[1] > 1 else page
-    os_ = t.stride(0) * es if t.shape[0] > 1 else ps * num_pages
-    return _ptr(t), t.shape[0], os_, ps, page
+    ps = st[1] * es if num_pages > 1 else page
+    return t.data_ptr(), shape[0], st[0] * es if shape[0] > 1 else ps * num_pages, ps, page
 
 
 def pages_reserve(table, length, ref, rows, new_length, page_size, *, info=None, stream=None):
     """Grows rows (int32 [n]) to new_length (int32 [n]), with the lowest-numbered free pages
     in the list's order; in place.  info int32 [1], when given, receives the free pages left,
     or minus the number missing, and then nothing has changed."""
-    ctx, stream = _on(table, stream)
-    dev = table.device
-    R, P, num_pages = _cache(table, length, ref, dev)
-    n = rows.numel()
-    _check_on(rows, "rows", torch.int32, (n,), dev)
-    _check_on(new_length, "new_length", torch.int32, (n,), dev)
-    if info is not None:
-        _check_on(info, "info", torch.int32, (1,), dev)
-    with ctx:
-        rc = load().kda_pages_reserve(_ptr(table), _ptr(length), _ptr(ref), _ptr(rows), _ptr(new_length), n, _ptr(info),
-                                      R, P, num_pages, int(page_size), ctypes.c_void_p(stream.cuda_stream))
+    if not _here(table, stream):
+        with _there(table, stream):
+            return pages_reserve(table, length, ref, rows, new_length, page_size, info=info)
+    dev, n = table.device, rows.numel()
+    t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
+    rc = load().kda_pages_reserve(t, ln, rf, _arr(rows, "rows", torch.int32, (n,), dev),
+                                  _arr(new_length, "new_length", torch.int32, (n,), dev), n, inf, R, P, pages, page_size,
+                                  _raw_stream(table))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_reserve")
 
@@ -680,40 +698,34 @@ def pages_fork(table, length, ref, src, dst, page_size, *, pools=(), info=None, 
     """Empty rows dst (int32 [n]) share the sequences of rows src: full pages by count, a
     partial last page copied in every pool [outer, num_pages, ...].  Returns (copy_src,
     copy_dst), int32 [n], the pages copied (-1, -1: none).  info as ``pages_reserve``."""
-    ctx, stream = _on(table, stream)
-    dev = table.device
-    R, P, num_pages = _cache(table, length, ref, dev)
-    n = src.numel()
-    _check_on(src, "src", torch.int32, (n,), dev)
-    _check_on(dst, "dst", torch.int32, (n,), dev)
-    if info is not None:
-        _check_on(info, "info", torch.int32, (1,), dev)
-    args = [_pool(t, num_pages, dev) for t in pools]
-    with ctx:
-        pairs = torch.empty((2, n), device=dev, dtype=torch.int32)
-        cs, cd = pairs[0], pairs[1]
-        st = ctypes.c_void_p(stream.cuda_stream)
-        rc = load().kda_pages_fork(_ptr(table), _ptr(length), _ptr(ref), _ptr(src), _ptr(dst), n, _ptr(cs), _ptr(cd),
-                                   _ptr(info), R, P, num_pages, int(page_size), st)
+    if not _here(table, stream):
+        with _there(table, stream):
+            return pages_fork(table, length, ref, src, dst, page_size, pools=pools, info=info)
+    dev, n = table.device, src.numel()
+    t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
+    args = [_pool(x, pages, dev) for x in pools]
+    a, b = _arr(src, "src", torch.int32, (n,), dev), _arr(dst, "dst", torch.int32, (n,), dev)
+    cs, cd = torch.empty((2, n), device=dev, dtype=torch.int32).unbind(0)
+    lib, st = load(), _raw_stream(table)
+    rc = lib.kda_pages_fork(t, ln, rf, a, b, n, cs.data_ptr(), cd.data_ptr(), inf, R, P, pages, page_size, st)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_pages_fork")
+    for x in args:
+        rc = lib.kda_pages_copy(*x, pages, cs.data_ptr(), cd.data_ptr(), n, st)
         if rc != KDA_OK:
-            raise KdaError(rc, "kda_pages_fork")
-        for a in args:
-            rc = load().kda_pages_copy(*a, num_pages, _ptr(cs), _ptr(cd), n, st)
-            if rc != KDA_OK:
-                raise KdaError(rc, "kda_pages_copy")
+            raise KdaError(rc, "kda_pages_copy")
     return cs, cd
 
 
 def pages_free(table, length, ref, rows, page_size, *, stream=None):
     """Ends the sequences of rows (int32 [n]), in place."""
-    ctx, stream = _on(table, stream)
-    dev = table.device
-    R, P, num_pages = _cache(table, length, ref, dev)
-    n = rows.numel()
-    _check_on(rows, "rows", torch.int32, (n,), dev)
-    with ctx:
-        rc = load().kda_pages_free(_ptr(table), _ptr(length), _ptr(ref), _ptr(rows), n, R, P, num_pages, int(page_size),
-                                   ctypes.c_void_p(stream.cuda_stream))
+    if not _here(table, stream):
+        with _there(table, stream):
+            return pages_free(table, length, ref, rows, page_size)
+    dev, n = table.device, rows.numel()
+    t, ln, rf, _, R, P, pages = _cache(table, length, ref, None, dev)
+    rc = load().kda_pages_free(t, ln, rf, _arr(rows, "rows", torch.int32, (n,), dev), n, R, P, pages, page_size,
+                               _raw_stream(table))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_free")
 
@@ -722,43 +734,38 @@ def pages_compact(table, length, ref, page_size, *, table_out=None, ref_out=None
     """Moves the live pages of every pool [outer, num_pages, ...] to the front and renumbers
     table and ref, in place or into table_out and ref_out.  Returns (table, ref) as written;
     info int32 [1], when given, receives the number of free pages."""
-    ctx, stream = _on(table, stream)
+    if not _here(table, stream):
+        with _there(table, stream):
+            return pages_compact(table, length, ref, page_size, table_out=table_out, ref_out=ref_out, pools=pools, info=info)
     dev = table.device
-    R, P, num_pages = _cache(table, length, ref, dev)
+    t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
     table_out = table if table_out is None else table_out
     ref_out = ref if ref_out is None else ref_out
-    _check_on(table_out, "table_out", torch.int32, (R, P), dev)
-    _check_on(ref_out, "ref_out", torch.int32, (num_pages,), dev)
-    if info is not None:
-        _check_on(info, "info", torch.int32, (1,), dev)
-    args = [_pool(t, num_pages, dev) for t in pools]
-    with ctx:
-        nbytes = int(load().kda_pages_compact_workspace_bytes(num_pages))
-        ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
-        st = ctypes.c_void_p(stream.cuda_stream)
-        rc = load().kda_pages_compact(_ptr(table), _ptr(length), _ptr(ref), _ptr(table_out), _ptr(ref_out), _ptr(info),
-                                      R, P, num_pages, int(page_size), _ptr(ws), nbytes, st)
+    to, ro = _arr(table_out, "table_out", torch.int32, (R, P), dev), _arr(ref_out, "ref_out", torch.int32, (pages,), dev)
+    args = [_pool(x, pages, dev) for x in pools]
+    lib, st = load(), _raw_stream(table)
+    nbytes = lib.kda_pages_compact_workspace_bytes(pages)
+    ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+    rc = lib.kda_pages_compact(t, ln, rf, to, ro, inf, R, P, pages, page_size, ws.data_ptr(), nbytes, st)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_pages_compact")
+    for x in args:
+        rc = lib.kda_pages_compact_pool(*x, pages, ws.data_ptr(), nbytes, st)
         if rc != KDA_OK:
-            raise KdaError(rc, "kda_pages_compact")
-        for a in args:
-            rc = load().kda_pages_compact_pool(*a, num_pages, _ptr(ws), nbytes, st)
-            if rc != KDA_OK:
-                raise KdaError(rc, "kda_pages_compact_pool")
+            raise KdaError(rc, "kda_pages_compact_pool")
     return table_out, ref_out
 
 
 def pages_copy(pool, src, dst, *, stream=None):
     """pool[:, dst[i]] = pool[:, src[i]] for int32 [n] src, dst, on a pool [outer, num_pages, ...]
     with contiguous pages: key/value pages of every layer, or recurrent states in slots."""
-    ctx, stream = _on(pool, stream)
-    dev = pool.device
+    if not _here(pool, stream):
+        with _there(pool, stream):
+            return pages_copy(pool, src, dst)
     if pool.dim() < 3:
         raise ValueError("a pool must be [outer, num_pages, ...]")
-    a = _pool(pool, pool.shape[1], dev)
-    n = src.numel()
-    _check_on(src, "src", torch.int32, (n,), dev)
-    _check_on(dst, "dst", torch.int32, (n,), dev)
-    with ctx:
-        rc = load().kda_pages_copy(*a, pool.shape[1], _ptr(src), _ptr(dst), n, ctypes.c_void_p(stream.cuda_stream))
+    dev, pages, n = pool.device, pool.shape[1], src.numel()
+    rc = load().kda_pages_copy(*_pool(pool, pages, dev), pages, _arr(src, "src", torch.int32, (n,), dev),
+                               _arr(dst, "dst", torch.int32, (n,), dev), n, _raw_stream(pool))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_copy")
