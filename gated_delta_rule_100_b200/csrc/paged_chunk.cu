@@ -25,13 +25,19 @@
 // sixteen by the time it models for all SMs, longest items first; CTAs, one per
 // SM, claim pieces from a counter.  Pieces of a split item are joined by
 // paged_join_kernel in a fixed order.
+#include <type_traits>
+
 #include "kda_internal.cuh"
 #include "paged_params.cuh"
 
 namespace kda {
 
-constexpr int CK_M = 128, CK_KT = 128, CK_ROWS = 2 * CK_M;  // rows of a tile, keys of a tile, rows of an item
-constexpr int CK_THREADS = 320, CK_MMA = 8, CK_LOAD = 9;    // warps 0-7: rows; 8: products; 9: loads
+constexpr int CK_M = 128, CK_KT = 128, CK_ROWS = 2 * CK_M;  // rows of a tile, keys of a loaded tile, rows of an item
+constexpr int CK_STEP = 64;                                  // keys whose weights are formed at a time
+constexpr int CK_RW = 8;                                     // warps of rows, four a tile
+constexpr int CK_MMA = CK_RW, CK_LOAD = CK_RW + 1;           // one for the products, one for the loads, two idle
+constexpr int CK_THREADS = (CK_RW + 4) * 32;
+constexpr int CK_REGS_ROWS = 216, CK_REGS_REST = 72;         // 256 x 216 + 128 x 72 = 384 x 168, the launch's registers
 
 // One piece of work: keys [kv0, kv1) in tiles of rows [t 256, t 256 + 256) of
 // (n, h); part_row: where its partial sums go, or -1 when it is the whole item.
@@ -47,18 +53,21 @@ struct ChunkParams {
     PagedParams p;
     ChunkPlanHead *head;
     ChunkPiece *pieces;
-    int *base;             // [N] the plan's scratch
+    int2 *base;            // [N] the plan's scratch
     int max_pieces, max_entries, max_rows, sms;
 };
 
 template <int D>
 struct CkShape {
     static constexpr int TILE = CK_KT * D * 2;                    // a key or value tile
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int OFF_RING = 2 * CK_M * D * 2;             // behind the two query tiles
-    static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
-    static constexpr int B_Q = 0, B_S = 1, B_P = 3, B_TAIL = 5, B_DRAIN = 6, B_FULL = 7, B_EMPTY = B_FULL + STAGES, NBAR = B_EMPTY + STAGES;
-    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;        // and room to align the base
+    // two stages of keys, then two of values
+    static constexpr int OFF_K = 2 * CK_M * D * 2, OFF_V = OFF_K + 2 * TILE;  // behind the two query tiles
+    static constexpr int OFF_BAR = OFF_V + 2 * TILE;
+    // barriers: queries [tile], scores [tile], weights [tile][half], a half's products [tile], a pair of tiles loaded [stage],
+    // read [stage], a tail's copies, the end of all products, pieces handed on [2], taken [2]
+    static constexpr int B_Q = 0, B_S = 2, B_P = 4, B_HALF = 8, B_FULL = 10, B_EMPTY = 12, B_TAIL = 14, B_DRAIN = 15, B_WORK = 16,
+                         B_FREE = 18, NBAR = 20;
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;          // and four words
     static constexpr uint32_t TM_S = 0, TM_O = 256;               // columns: S0, S1, O0, O1
 };
 
@@ -70,114 +79,168 @@ __device__ __forceinline__ int ck_keys(const PagedSeq &s, int G, int t) {  // ke
 // rows that row tile t holds
 __device__ __forceinline__ int ck_rows(const PagedSeq &s, int G, int t) { return min(CK_ROWS, s.nq * G - t * CK_ROWS); }
 
+// Cutting the items.  In each sequence the row tiles with the most keys stay
+// whole (a share `phi` of the tiles: none, or as many as fill whole waves of
+// SMs), the others are cut into pieces of `step` key tiles, one of sixteen
+// divisors of the longest.  The 32 candidates are compared by a modelled time in
+// key tiles: a piece costs its tiles and about three more; the whole items' waves
+// first, their last wave's idle SMs already at the pieces; then the pieces' waves;
+// and the join of what was cut, at the memory's rate.
 constexpr int CK_CAND = 16;
 __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64, 128, 256};
 
 __device__ void ck_plan(const ChunkParams &c, int d) {
-    __shared__ unsigned long long s_w;
-    __shared__ unsigned long long s_pieces[CK_CAND], s_rows[CK_CAND];
-    __shared__ int s_max, s_step, s_entries, s_part, s_sum[33];
+    __shared__ unsigned long long s_w, s_wa, s_pieces[2][CK_CAND], s_rows[2][CK_CAND];
+    __shared__ int s_max, s_items, s_a, s_step, s_phi, s_entries, s_part, s_sum[2][33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
-    if (tid == 0) { s_w = 0; s_max = 1; s_entries = 0; s_part = 0; }
-    if (tid < CK_CAND) s_pieces[tid] = s_rows[tid] = 0;
+    if (tid == 0) { s_w = s_wa = 0; s_max = 1; s_items = s_a = s_entries = s_part = 0; }
+    if (tid < 2 * CK_CAND) s_pieces[tid / CK_CAND][tid % CK_CAND] = s_rows[tid / CK_CAND][tid % CK_CAND] = 0;
     __syncthreads();
     // a warp a sequence, a lane a row tile
     unsigned long long w = 0;
-    int mx = 1;
+    int mx = 1, items = 0;
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, lane == 0);
         for (int t = lane; t < ck_tiles(s, G); t += 32) {
             const int k = ck_keys(s, G, t);
             w += k;
             mx = max(mx, k);
+            ++items;
         }
     }
-    atomicAdd(&s_w, w);
-    atomicMax(&s_max, mx);
+    // a warp's sum first: 32 lanes' atomics on one 64-bit word of shared memory wait for one another
+    auto warp_sum = [](unsigned long long v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    w = warp_sum(w);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    items = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 0 && items) {
+        atomicAdd(&s_w, w);
+        atomicMax(&s_max, mx);
+        atomicAdd(&s_items, items);
+    }
     __syncthreads();
-    int pieces[CK_CAND] = {};
-    unsigned long long rows[CK_CAND] = {};
+    const long long all = (long long)s_items * p.Hkv;
+    const float phi1 = (float)(all / c.sms * c.sms) / fmaxf((float)all, 1.f);
+    // whole tiles of a sequence: ranks below, counted from the one with the most keys
+    auto whole = [&](int tiles, int phi) { return phi ? (int)(tiles * phi1) : 0; };
+    int pieces[2][CK_CAND] = {};
+    unsigned rows[2][CK_CAND] = {};  // of one head; 2^32 of them would take 2 TB
+    unsigned long long wa = 0;
+    int na = 0;
+    float inv[CK_CAND];
+#pragma unroll
+    for (int j = 0; j < CK_CAND; ++j) inv[j] = 1.f / ((s_max + ck_div[j] - 1) / ck_div[j]);
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, false);
-        for (int t = lane; t < ck_tiles(s, G); t += 32) {
+        const int tiles = ck_tiles(s, G);
+        for (int t = lane; t < tiles; t += 32) {
             const int k = ck_keys(s, G, t), r = ck_rows(s, G, t);
+            const bool a = tiles - 1 - t < whole(tiles, 1);
+            if (a) { wa += k; ++na; }
 #pragma unroll
             for (int j = 0; j < CK_CAND; ++j) {
-                const int step = (s_max + ck_div[j] - 1) / ck_div[j], ns = (k + step - 1) / step;
-                pieces[j] += ns;
-                if (ns > 1) rows[j] += (unsigned long long)ns * r;
+                const int ns = (int)ceilf(k * inv[j] - 1e-3f);  // near enough for the choice
+                pieces[0][j] += ns;
+                if (ns > 1) rows[0][j] += (unsigned)ns * r;
+                if (!a) {
+                    pieces[1][j] += ns;
+                    if (ns > 1) rows[1][j] += (unsigned)ns * r;
+                }
             }
         }
     }
+    if (items) {  // the same in every lane
 #pragma unroll
-    for (int j = 0; j < CK_CAND; ++j) {
-        atomicAdd(&s_pieces[j], (unsigned long long)pieces[j]);
-        atomicAdd(&s_rows[j], rows[j]);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < CK_CAND; ++j) {
+                const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)pieces[q][j]), b = __reduce_add_sync(0xffffffffu, rows[q][j]);
+                if (lane == 0) {
+                    atomicAdd(&s_pieces[q][j], (unsigned long long)a);
+                    atomicAdd(&s_rows[q][j], (unsigned long long)b);
+                }
+            }
+        wa = warp_sum(wa);
+        na = __reduce_add_sync(0xffffffffu, na);
+        if (lane == 0) {
+            atomicAdd(&s_wa, wa);
+            atomicAdd(&s_a, na);
+        }
     }
     __syncthreads();
     if (warp == 0) {
-        // modelled time in key tiles: the waves of pieces, each with a fixed cost of about
-        // three tiles, no less than the longest piece; joins at the memory's rate
-        float cost = 3.0e38f;
-        int step = s_max;
-        if (lane < CK_CAND) {
-            step = (s_max + ck_div[lane] - 1) / ck_div[lane];
-            const float P = (float)s_pieces[lane] * p.Hkv, W = (float)s_w * p.Hkv, R = (float)s_rows[lane] * p.Hkv;
-            const float waves = ceilf(P / c.sms);
-            if (lane == 0 || (P <= c.max_pieces && R <= c.max_rows))
-                cost = fmaxf(waves * (W / P + 3.f), step + 3.f) + (R > 0.f ? 3.f + R * d * 8.f * 1.2e-7f : 0.f);
-        }
+        const int q = lane / CK_CAND, j = lane % CK_CAND, step = (s_max + ck_div[j] - 1) / ck_div[j];
+        const float S = (float)c.sms, R = (float)s_rows[q][j] * p.Hkv;
+        const float pa = q ? (float)s_a * p.Hkv : 0.f, ta = q && s_a ? (float)s_wa / s_a + 3.f : 0.f;
+        const float pb = (float)s_pieces[q][j] * p.Hkv, tb = pb > 0.f ? (float)(s_w - (q ? s_wa : 0)) * p.Hkv / pb + 3.f : 3.f;
+        const float ka = ceilf(pa / S), early = (ka * S - pa) * floorf(ta / tb);
+        float cost = ka * ta + (pb > early ? fmaxf(ceilf((pb - early) / S) * tb, fminf(step + 3.f, tb * 2.f)) : 0.f);
+        if (R > 0.f) cost += 3.f + R * d * 8.f * 1.2e-7f;
+        if (lane > 0 && (pa + pb > c.max_pieces || R > c.max_rows)) cost = 3.0e38f;
         float best = cost;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
         const int who = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
-        step = __shfl_sync(0xffffffffu, step, who);
-        if (lane == 0) s_step = step;
+        if (lane == who) { s_step = step; s_phi = q; }
     }
     __syncthreads();
-    const int step = s_step;
-    // pieces of each sequence and key head, then where each sequence's begin
+    const int step = s_step, phi = s_phi;
+    // pieces per key head of a sequence, whole ones and others; then where each sequence's begin:
+    // every whole item first
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, false);
+        const int tiles = ck_tiles(s, G), a = whole(tiles, phi);
         int k = 0;
-        for (int t = lane; t < ck_tiles(s, G); t += 32) k += (ck_keys(s, G, t) + step - 1) / step;
+        for (int t = lane; t < tiles - a; t += 32) k += (ck_keys(s, G, t) + step - 1) / step;
         k = __reduce_add_sync(0xffffffffu, k);
-        if (lane == 0) c.base[n] = k * p.Hkv;
+        if (lane == 0) c.base[n] = make_int2(a * p.Hkv, k * p.Hkv);
     }
     __syncthreads();
     const int per = (p.N + blockDim.x - 1) / blockDim.x;
-    int mine = 0;
-    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) mine += c.base[n];
-    int incl = mine;
+    int mine[2] = {0, 0}, at[2], total[2] = {0, 0};
+    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) { mine[0] += c.base[n].x; mine[1] += c.base[n].y; }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+    for (int q = 0; q < 2; ++q) {
+        int incl = mine[q];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s_sum[q][warp] = incl;
+        at[q] = incl - mine[q];
     }
-    if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    int at = incl - mine, total = 0;
-    for (int k = 0; k < warps; ++k) {
-        if (k < warp) at += s_sum[k];
-        total += s_sum[k];
-    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        for (int k = 0; k < warps; ++k) {
+            if (k < warp) at[q] += s_sum[q][k];
+            total[q] += s_sum[q][k];
+        }
+    at[1] += total[0];
     for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) {
-        const int k = c.base[n];
-        c.base[n] = at;
-        at += k;
+        const int2 k = c.base[n];
+        c.base[n] = make_int2(at[0], at[1]);
+        at[0] += k.x;
+        at[1] += k.y;
     }
     __syncthreads();
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, false);
-        const int tiles = ck_tiles(s, G);
-        const int first = c.base[n], head_pieces = (n + 1 < p.N ? c.base[n + 1] : total) - first;
-        const int per_head = head_pieces / p.Hkv;
+        const int tiles = ck_tiles(s, G), a = whole(tiles, phi);
+        const int2 first = c.base[n];
+        const int per_head = ((n + 1 < p.N ? c.base[n + 1].y : total[0] + total[1]) - first.y) / p.Hkv;
         int before = 0;
         for (int t0 = 0; t0 < tiles; t0 += 32) {
-            const int t = tiles - 1 - (t0 + lane);  // the longest first
-            const int k = t >= 0 ? ck_keys(s, G, t) : 0, ns = t >= 0 ? (k + step - 1) / step : 0;
-            int inc = ns;
+            const int rank = t0 + lane, t = tiles - 1 - rank;  // the longest first
+            const bool w1 = rank < a;
+            const int k = t >= 0 ? ck_keys(s, G, t) : 0, st = w1 ? k : step, ns = t >= 0 ? (k + st - 1) / st : 0;
+            int inc = w1 ? 0 : ns;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -186,7 +249,7 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
             if (t >= 0) {
                 const int r = ck_rows(s, G, t);
                 for (int h = 0; h < p.Hkv; ++h) {
-                    const long long i = (long long)first + (long long)h * per_head + before + inc - ns;
+                    const long long i = w1 ? first.x + (long long)h * a + rank : first.y + (long long)h * per_head + before + inc - ns;
                     int part = -1;
                     if (ns > 1) {
                         part = atomicAdd(&s_part, ns * r);
@@ -200,7 +263,7 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
                         const int row = part < 0 ? -1 : part + j * r;
                         // a piece without room for its sums is left empty
                         const bool room = part < 0 || part + ns * r <= c.max_rows;
-                        c.pieces[i + j] = {n, h, t, j * step, room ? min(k, (j + 1) * step) : j * step, row, {0, 0}};
+                        c.pieces[i + j] = {n, h, t, j * st, room ? min(k, (j + 1) * st) : j * st, row, {0, 0}};
                     }
                 }
             }
@@ -209,7 +272,7 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     }
     __syncthreads();
     if (tid == 0) {
-        c.head->pieces = min(total, c.max_pieces);
+        c.head->pieces = min(total[0] + total[1], c.max_pieces);
         c.head->ticket = 0;
         c.head->entries = min(s_entries, c.max_entries);
     }
@@ -246,6 +309,21 @@ __global__ void __launch_bounds__(512) paged_plan_kernel(const ChunkParams c) {
     else ck_append<D>(c, (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x, (long long)(gridDim.x - 1) * blockDim.x);
 }
 
+// A bounded wait of at most `tries` tries, in five instructions.  mbar_wait reads
+// %globaltimer after its first miss, which takes longer than most waits here (it
+// cost each contended wait 300 to 600 cycles), and is long where the
+// instruction cache is short of room.
+__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+        "again_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done_%=;\n\t"
+        "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra again_%=;\n"
+        "done_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(tries) : "memory");
+    return ok != 0;
+}
+
 // -------------------------------------------------------------- tensor memory ----
 __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t *r) {
     asm volatile(
@@ -267,190 +345,365 @@ __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t *r) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] B[smem]: A's rows are lanes, two 16-bit values a column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The products, with descriptors by their low word (address and leading stride);
+// the high word is the same for all of them here: 1024 bytes between 8-row atoms,
+// 128-byte swizzle.  Few instructions between products count: the issuing warp
+// runs alone, at some ten cycles each.
+constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | (lead >> 4) << 16; }
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
         : "memory");
 }
+// D[tmem] (+)= A[tmem] B[smem]: A's rows are lanes, two 16-bit values a column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+        : "memory");
+}
+
+// One lane of a converged warp.  The compiler knows that the branch on it holds
+// for a single lane, and keeps descriptors in uniform registers: products issued
+// under `lane == 0` cost 73 to 87 cycles each, under this 64, the tensor
+// cores' own time for 128 x 128 x 16.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// 2^x without the exponential unit, for x = s sc - ref: y = (x + 120) / 128 in one
+// operation that also holds it in [0, 1] (x in [-120, 8]); x = n + r with n the
+// nearest integer (128 y - 120 added to 1.5 2^23, whose last place is 1, leaves n
+// in the low bits) and r in [-1/2, 1/2]; 2^r by the polynomial of degree 4 with
+// the least largest relative error there, 2.7e-6 (a least-squares fit with its
+// weights moved to the error's peaks); n added to the exponent.  y's last place
+// is another 2.6e-6; a weight's 16-bit rounding is 100 times both.  A score far
+// below the maximum weighs 2^-120 and not 0: not for masked keys.
+struct PolyScale {
+    float a, b;  // y = s a + b
+};
+__device__ __forceinline__ PolyScale poly_scale(float sc, float ref) { return {sc * 0.0078125f, (120.f - ref) * 0.0078125f}; }
+__device__ __forceinline__ float exp2_poly(float s, const PolyScale &k) {
+    constexpr float shift = 12582912.f - 120.f;
+    float y;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(s), "f"(k.a), "f"(k.b));
+    const float t = fmaf(y, 128.f, shift);
+    const float r = fmaf(y, 128.f, shift - t);
+    float q = fmaf(r, 0.0095701003447f, 0.0559178590775f);
+    q = fmaf(q, r, 0.2402474433184f);
+    q = fmaf(q, r, 0.6931217908859f);
+    q = fmaf(q, r, 0.9999992847443f);
+    return __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));
+}
+
+// Weights 2^(x sc - ref) of a row's 64 scores as 16-bit pairs, and their sum
+// before the rounding.  MIX: one of eight by the polynomial, which makes up for
+// the exponential unit's rate (512 cycles a warp for 64; so 384 and the FMA
+// pipe's share beside it); it has no 0 for masked keys.
+template <bool BF, bool MIX>
+__device__ __forceinline__ float ck_weights(const uint32_t (&x)[CK_STEP], uint32_t (&y)[CK_STEP / 2], float sc, float ref) {
+    const PolyScale ps = poly_scale(sc, ref);
+    float l[4] = {};
+#pragma unroll
+    for (int k = 0; k < CK_STEP; k += 2) {
+        const float u = __uint_as_float(x[k]), v = __uint_as_float(x[k + 1]);
+        const float a = ex2(fmaf(u, sc, -ref));
+        const float b = MIX && k % 8 == 0 ? exp2_poly(v, ps) : ex2(fmaf(v, sc, -ref));
+        l[k & 2] += a;
+        l[(k & 2) + 1] += b;
+        y[k / 2] = pack16x2<BF>(a, b);
+    }
+    return (l[0] + l[1]) + (l[2] + l[3]);
+}
+
+// The issuing lane's walk over a piece.  Its loop holds the steps of one key tile
+// and no more: it runs alone, at some ten cycles an instruction, so a loop
+// over the steps cost 400 cycles each; and the instruction cache that it shares
+// with two of the rows' warps is short, so unrolled over the stages too it slowed
+// those two by half.
+template <int D, bool BF>
+struct Issuer {
+    using S = CkShape<D>;
+    uint32_t base, tmem, tries;
+    uint32_t q_par0 = 0, q_par1 = 0, p_par0 = 0, p_par1 = 0, f_par = 0;  // parities waited for next
+
+    __device__ __forceinline__ uint32_t bar(int i) const { return base + S::OFF_BAR + i * 8; }
+    template <int W>
+    __device__ __forceinline__ void scores(uint32_t k) const {  // S[W] = Q[W] K^T, k: the key tile's descriptor
+        constexpr uint32_t idesc = make_idesc(BF ? 1 : 0, false, false, CK_M, CK_KT);
+        uint32_t q = desc_lo(base, 16) + W * (CK_M * D * 2 / 16);
+        asm volatile("" : "+r"(q), "+r"(k));  // the products' descriptors are formed here, not kept
+#pragma unroll
+        for (int e = 0; e < D; e += 16) {
+            constexpr int KB = CK_KT * 128 / 16;  // 16-byte units of 64 channels
+            umma_ss(tmem + S::TM_S + W * 128, q + e / 64 * KB + e % 64 / 8, k + e / 64 * KB + e % 64 / 8, idesc, e > 0);
+        }
+    }
+    template <int W, int H>
+    __device__ __forceinline__ bool values(uint32_t v, bool add) const {  // O[W] (+)= P[W][H] V, half H of the value tile
+        constexpr uint32_t idesc = make_idesc(BF ? 1 : 0, false, true, CK_M, D);
+        if (!ck_wait(bar(S::B_P + W * 2 + H), W ? p_par1 : p_par0, tries)) return false;
+        tc_fence_after();
+        asm volatile("" : "+r"(v));
+#pragma unroll
+        for (int e = 0; e < CK_STEP; e += 16)
+            umma_ts(tmem + S::TM_O + W * D, tmem + S::TM_S + W * 128 + (H * CK_STEP + e) / 2, v + (H * CK_STEP + e) * 128 / 16, idesc,
+                    H || e ? 1u : (uint32_t)add);
+        return true;
+    }
+    // a tile's weights times their values as the halves come, then its scores of the next keys
+    template <int W>
+    __device__ __forceinline__ bool step(uint32_t v, uint32_t k, bool add, bool more) const {
+        if (!values<W, 0>(v, add)) return false;
+        umma_commit(bar(S::B_HALF + W));
+        if (!values<W, 1>(v, true)) return false;
+        if (more) scores<W>(k);
+        umma_commit(bar(S::B_S + W));  // and every product before it
+        return true;
+    }
+    // Tiles come in pairs, the values of key tile i with the keys of tile i + 1: that is what
+    // tile i's steps read, so one barrier says that both are there and one that both are free.
+    // The pair of tile i is in stage (i + 1) & 1; its values lie in that stage of their ring, its
+    // keys in the other.  A piece's first pair is its first keys alone, and it takes an even
+    // number of pairs (the last one empty if need be), so that it begins at stage 0.
+    __device__ __forceinline__ bool full(uint32_t st) {
+        if (!ck_wait(bar(S::B_FULL) + st * 8, f_par, tries)) return false;
+        f_par ^= st;
+        return true;
+    }
+    __device__ __forceinline__ bool run(int nt, bool both) {
+        const uint32_t k0 = desc_lo(base + S::OFF_K, 16), v0 = desc_lo(base + S::OFF_V, CK_KT * 128);
+        if (!full(0) || !ck_wait(bar(S::B_Q), q_par0, tries)) return false;
+        q_par0 ^= 1;
+        tc_fence_after();
+        scores<0>(k0 + S::TILE / 16);
+        umma_commit(bar(S::B_S));
+        if (both) {
+            if (!ck_wait(bar(S::B_Q + 1), q_par1, tries)) return false;
+            q_par1 ^= 1;
+            tc_fence_after();
+            scores<1>(k0 + S::TILE / 16);
+            umma_commit(bar(S::B_S + 1));
+        }
+        umma_commit(bar(S::B_EMPTY));
+        uint32_t st = 1;
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i, st ^= 1) {
+            const uint32_t v = v0 + st * (S::TILE / 16), k = k0 + (st ^ 1) * (S::TILE / 16);
+            const bool more = i + 1 < nt;
+            if (!full(st) || !step<0>(v, k, i > 0, more)) return false;
+            if (both && !step<1>(v, k, i > 0, more)) return false;
+            umma_commit(bar(S::B_EMPTY) + st * 8);
+            p_par0 ^= 1;
+            p_par1 ^= (uint32_t)both;
+        }
+        if ((nt & 1) == 0) {  // the empty pair
+            if (!full(1)) return false;
+            umma_commit(bar(S::B_EMPTY + 1));
+        }
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------ kernel ----
 template <int D, bool BF>
 __global__ void __launch_bounds__(CK_THREADS, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ChunkParams c) {
     using S = CkShape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_piece;
-    __shared__ volatile int s_abort;
+    extern __shared__ __align__(1024) uint8_t sm[];  // swizzle atoms are 1024 bytes
     const PagedParams &p = c.p;
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t *sm = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t base = smem_u32(sm);
+    volatile int *words = reinterpret_cast<volatile int *>(sm + S::OFF_BAR + S::NBAR * 8);
+    volatile int *s_piece = words;       // [2] the pieces handed on
+    volatile int &s_abort = words[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.G;
-    const uint64_t polls = p.st.wait_polls;
+    const uint32_t tries = p.st.wait_polls < (1u << 20) ? (uint32_t)p.st.wait_polls : 1u << 20;  // of some 50 ns up
     auto bar = [&](int i) { return base + S::OFF_BAR + i * 8; };
 
     if (tid == 0) {
-        for (int i = 0; i < S::NBAR; ++i) mbar_init(bar(i), i == S::B_Q ? 8u : (i >= S::B_P && i < S::B_P + 2) ? 4u : 1u);
+        for (int i = 0; i < S::NBAR; ++i)
+            mbar_init(bar(i), (i < S::B_S || (i >= S::B_P && i < S::B_P + 4)) ? 4u : (i == S::B_FREE || i == S::B_FREE + 1) ? CK_RW + 1u : 1u);
         s_abort = 0;
         fence_mbar_init();
     }
     if (warp == CK_MMA) {
-        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_alloc(base + S::OFF_BAR + S::NBAR * 8 + 12, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = (uint32_t)words[3];
     const int pieces = c.head->pieces;
-
     auto wait1 = [&](int i, uint32_t par) -> bool {
-        if (mbar_wait(bar(i), par, polls, p.st)) return true;
+        if (ck_wait(bar(i), par, tries)) return true;
         s_abort = 1;
+        report(p.st, DEV_TIMEOUT);
         return false;
     };
     auto wait_warp = [&](int i, uint32_t par) -> bool {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(i), par, polls, p.st));
-        if (!ok) s_abort = 1;
+        const bool ok = __all_sync(0xffffffffu, ck_wait(bar(i), par, tries));
+        if (!ok) {
+            s_abort = 1;
+            report(p.st, DEV_TIMEOUT);
+        }
         return ok;
     };
     auto arrive1 = [&](int i) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(i)) : "memory"); };
 
-    uint32_t done = 0;          // pieces with work that this CTA has finished (completions of B_Q)
-    uint32_t tick = 0;          // ring tiles loaded (loader) or read (issuer) so far
-    uint32_t s_phase = 0;       // rows: completions of this tile's B_S so far
-    uint32_t p_phase0 = 0, p_phase1 = 0;  // issuer: completions of B_P
-    uint32_t tails = 0;         // loader: completions of B_TAIL
+    // The loader claims pieces and hands each on through two slots, so that it can run ahead:
+    // it loads the next piece's keys while the rows of this one are being finished.
+    // take(): the k-th piece (-1: no more); a warp is done with its slot once it has read it.
+    auto take = [&](uint32_t k) -> int {
+        if (!wait_warp(S::B_WORK + (k & 1), (k >> 1) & 1)) return -1;
+        const int at = s_piece[k & 1];
+        __syncwarp();
+        if (lane == 0) arrive1(S::B_FREE + (k & 1));
+        return at;
+    };
 
-    for (;;) {
-        if (tid == 0) s_piece = atomicAdd(&c.head->ticket, 1);
-        __syncthreads();
-        const int at = s_piece;
-        if (at >= pieces || s_abort) break;
-        const ChunkPiece pc = c.pieces[at];
-        const PagedSeq sq = paged_seq(p, pc.n, false);
-        const int rows = ck_rows(sq, G, pc.t), nt = pc.kv1 - pc.kv0;
-        const int act = rows > CK_M ? 2 : 1;
-        const int first_new = sq.len - sq.nq;
-
-        if (nt <= 0) {
-            // nothing to do for this piece
-        } else if (warp == CK_LOAD) {
-            // ------------------------------------------------ loader (lane 0; all for the tail)
-            const int kv_end = paged_kv_end(sq, G, (pc.t + 1) * CK_ROWS - 1);
-            const int *trow = p.table + (long long)sq.row * p.P;
-            const int box = min(p.page_size, CK_KT);  // tokens of one copy
+    if (warp >= CK_RW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CK_REGS_REST));
+        if (warp == CK_LOAD) {
+            // ------------------------------------------------ loader
+            uint32_t g = 0, tails = 0;  // pairs begun, completions of B_TAIL
             bool ok = true;
-            for (int i = 0; ok && i < 2 * nt; ++i) {
-                const bool val = i & 1;
-                const int k0 = (pc.kv0 + (i >> 1)) * CK_KT;
-                const int st = tick % S::STAGES;
-                const uint32_t use = tick / S::STAGES;
-                const int valid = max(0, min(CK_KT, kv_end - k0));  // keys of the tile that some row sees
-                const int copies = (valid + box - 1) / box;
-                const bool tail = val && valid < CK_KT;
-                if (use > 0) ok = wait_warp(S::B_EMPTY + st, (use - 1) & 1);
-                if (!ok) break;
-                const uint32_t dst = base + S::OFF_RING + st * S::TILE;
-                const int bi = tail ? S::B_TAIL : S::B_FULL + st;
-                if (lane == 0) mbar_expect_tx(bar(bi), (uint32_t)copies * box * D * 2);
-                __syncwarp();
-                for (int k = lane; k < copies; k += 32) {
-                    const int pos = k0 + k * box;
-                    int page = trow[pos / p.page_size];
-                    if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); page = 0; }
-#pragma unroll
-                    for (int kb = 0; kb < D / 64; ++kb)
-                        tma_load_4d(dst + kb * CK_KT * 128 + k * box * 128, val ? &tm_v : &tm_k, bar(bi), kb * 64,
-                                    pos % p.page_size, pc.h, page);
+            for (uint32_t w = 0; ok; ++w) {
+                if (w >= 2 && !(ok = wait_warp(S::B_FREE + (w & 1), ((w >> 1) - 1) & 1))) break;
+                int at = 0;
+                if (lane == 0) {
+                    at = atomicAdd(&c.head->ticket, 1);
+                    if (at >= pieces || s_abort) at = -1;
+                    s_piece[w & 1] = at;
+                    arrive1(S::B_WORK + (w & 1));
                 }
-                if (tail) {  // rows behind the end become zeros before the products see them
-                    ok = wait_warp(S::B_TAIL, tails & 1);
-                    ++tails;
-                    for (int k = lane; k < (CK_KT - valid) * (D / 64) * 8; k += 32) {
-                        const int row = valid + k / (D / 64 * 8), kb = k / 8 % (D / 64), ch = k % 8;
-                        *reinterpret_cast<uint4 *>(sm + S::OFF_RING + st * S::TILE + kb * CK_KT * 128 + row * 128 + ch * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                if (at < 0) break;
+                const ChunkPiece pc = c.pieces[at];
+                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const int kv_end = paged_kv_end(sq, G, (pc.t + 1) * CK_ROWS - 1);
+                const int *trow = p.table + (long long)sq.row * p.P;
+                const int box = min(p.page_size, CK_KT);  // tokens of one copy
+                const int per_tile = CK_KT / box, per_page = p.page_size / box;  // copies of a tile, tiles of a page
+                int pi = pc.kv0 / per_page * per_tile, tok0 = pc.kv0 % per_page * CK_KT;  // page and token the tile begins at
+                // The row's page numbers, 32 at a time, a lane each, and the 32 after them: a table
+                // entry read when its tile is due would cost its latency for every 128 keys.
+                auto pages_at = [&](int i) { return trow[min(i + lane, p.P - 1)]; };
+                int window = pi & ~31, cur = pages_at(window), next = pages_at(window + 32);
+                const int cp = lane / (D / 64), kb = lane % (D / 64);  // a lane a copy and 64 channels
+                const int put = kb * CK_KT * 128 + cp * box * 128;
+                const int nt = pc.kv1 - pc.kv0;
+                if (nt <= 0) continue;
+                const int pairs = (nt + 2) & ~1;  // see Issuer
+                int vpage = 0, vtok = 0, vcopies = 0, vvalid = 0;  // the keys' tile of the pair before, whose values come now
+                for (int i = 0; ok && i < pairs; ++i, ++g) {
+                    const int st = g & 1;
+                    const int kt = pc.kv0 + i;
+                    const int valid = i < nt ? max(0, min(CK_KT, kv_end - kt * CK_KT)) : 0;  // keys of the tile that some row sees
+                    const int copies = (valid + box - 1) / box;
+                    if (i < nt && (pi & ~31) != window) {
+                        window += 32;
+                        cur = next;
+                        next = pages_at(window + 32);
                     }
-                    fence_async_smem();
+                    int page = __shfl_sync(0xffffffffu, cur, (pi & 31) + cp);
+                    if (cp < copies && (page < 0 || page >= p.num_pages)) { report(p.st, DEV_BAD_ARG); page = 0; }
+                    if (g >= 2 && !(ok = wait_warp(S::B_EMPTY + st, ((g >> 1) - 1) & 1))) break;
+                    // values behind the sequence's end become zeros before the products see them:
+                    // such a tile is a piece's last, and comes with no keys
+                    const bool tail = i > 0 && i <= nt && vvalid < CK_KT;
+                    const int bi = tail ? S::B_TAIL : S::B_FULL + st;
+                    if (lane == 0) mbar_expect_tx(bar(bi), (uint32_t)(vcopies + copies) * box * D * 2);
                     __syncwarp();
-                    if (lane == 0) arrive1(S::B_FULL + st);
+                    if (cp < vcopies) tma_load_4d(base + S::OFF_V + st * S::TILE + put, &tm_v, bar(bi), kb * 64, vtok, pc.h, vpage);
+                    if (cp < copies) tma_load_4d(base + S::OFF_K + (st ^ 1) * S::TILE + put, &tm_k, bar(bi), kb * 64, tok0, pc.h, page);
+                    if (tail) {
+                        ok = wait_warp(S::B_TAIL, tails & 1);
+                        ++tails;
+                        for (int k = lane; k < (CK_KT - vvalid) * (D / 64) * 8; k += 32) {
+                            const int row = vvalid + k / (D / 64 * 8), b = k / 8 % (D / 64), ch = k % 8;
+                            *reinterpret_cast<uint4 *>(sm + S::OFF_V + st * S::TILE + b * CK_KT * 128 + row * 128 + ch * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) arrive1(S::B_FULL + st);
+                    }
+                    vpage = page;
+                    vtok = tok0;
+                    vcopies = copies;
+                    vvalid = valid;
+                    if (per_page == 1) pi += per_tile;
+                    else if ((tok0 += CK_KT) == p.page_size) { tok0 = 0; ++pi; }
                 }
-                ++tick;
             }
             if (!ok && lane == 0)  // leave no copy in flight into this CTA's memory
-                for (uint32_t st = 0; st < S::STAGES && st < tick; ++st)
-                    mbar_wait(bar(S::B_FULL + st), ((tick + S::STAGES - 1 - st) / S::STAGES - 1) & 1, ~0ull, p.st);
+                for (uint32_t b = g >= 2 ? g - 2 : 0; b < g; ++b) mbar_wait(bar(S::B_FULL + (b & 1)), (b >> 1) & 1, ~0ull, p.st);
         } else if (warp == CK_MMA) {
-            // ------------------------------------------------ issuer (lane 0; the rest idle)
-            if (lane == 0) {
-                const uint32_t id_s = make_idesc(BF ? 1 : 0, false, false, CK_M, CK_KT);
-                const uint32_t id_o = make_idesc(BF ? 1 : 0, false, true, CK_M, D);
-                auto full = [&](uint32_t tk) { return wait1(S::B_FULL + tk % S::STAGES, (tk / S::STAGES) & 1); };
-                auto scores = [&](int w, uint32_t tk) {  // S[w] = Q[w] K^T
-                    const uint32_t qa = base + w * CK_M * D * 2, ka = base + S::OFF_RING + tk % S::STAGES * S::TILE;
-#pragma unroll
-                    for (int k = 0; k < D; k += 16)
-                        umma<0>(tmem + S::TM_S + w * 128, desc_kmaj<128, 2>(qa, CK_M, k), desc_kmaj<128, 2>(ka, CK_KT, k), id_s, k > 0);
-                };
-                auto values = [&](int w, uint32_t tk, bool add) {  // O[w] (+)= P[w] V
-                    const uint32_t va = base + S::OFF_RING + tk % S::STAGES * S::TILE;
-#pragma unroll
-                    for (int k = 0; k < CK_KT; k += 16)
-                        umma_ts(tmem + S::TM_O + w * D, tmem + S::TM_S + w * 128 + k / 2, desc_mnmaj<128>(va, CK_KT, k), id_o,
-                                add || k > 0);
-                };
-                bool ok = wait1(S::B_Q, done & 1) && full(tick);
-                if (ok) {
-                    tc_fence_after();
-                    for (int w = 0; w < act; ++w) {
-                        scores(w, tick);
-                        umma_commit(bar(S::B_S + w));
-                    }
-                    umma_commit(bar(S::B_EMPTY + tick % S::STAGES));
-                }
-                for (int i = 0; ok && i < nt; ++i) {
-                    const uint32_t kt = tick + 2 * i + 2, vt = tick + 2 * i + 1;
-                    const bool more = i + 1 < nt;
-                    if (!(ok = full(vt))) break;
-                    for (int w = 0; ok && w < act; ++w) {
-                        if (!(ok = wait1(S::B_P + w, ((w ? p_phase1 : p_phase0) + i) & 1))) break;
-                        tc_fence_after();
-                        values(w, vt, i > 0);
-                        if (w == act - 1) umma_commit(bar(S::B_EMPTY + vt % S::STAGES));
-                        if (more) {
-                            if (w == 0 && !(ok = full(kt))) break;
-                            scores(w, kt);
-                        }
-                        umma_commit(bar(S::B_S + w));
-                    }
-                    if (ok && more) umma_commit(bar(S::B_EMPTY + kt % S::STAGES));
-                }
-                if (!ok) {  // leave no product in flight
-                    umma_commit(bar(S::B_DRAIN));
-                    mbar_wait(bar(S::B_DRAIN), 0, ~0ull, p.st);
-                }
-            }
-            tick += 2 * nt;
-            p_phase0 += nt;
-            if (act == 2) p_phase1 += nt;
-            __syncwarp();
-        } else {
-            // ------------------------------------------------ rows: thread (w, r) owns one
-            const int w = warp >> 2, r = (warp & 3) * 32 + lane;
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const int row = w * CK_M + r;                           // in the item
-            const bool real = row < rows;
-            const int tok = (pc.t * CK_ROWS + row) / G, head = pc.h * G + (pc.t * CK_ROWS + row) % G;
+            // ------------------------------------------------ issuer (one lane issues)
+            Issuer<D, BF> is = {base, tmem, tries};
             bool ok = true;
-            {   // its query, to the swizzled tile
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (real ? (sq.q0 + tok) * p.q_ts + (long long)head * D : 0));
-                uint4 x[D / 8];
+            for (uint32_t k = 0; ok; ++k) {
+                const int at = take(k);
+                if (at < 0) break;
+                const ChunkPiece pc = c.pieces[at];
+                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const int nt = pc.kv1 - pc.kv0;
+                if (nt <= 0) continue;
+                if (elect_lane()) ok = is.run(nt, ck_rows(sq, G, pc.t) > CK_M);
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) {
+                s_abort = 1;
+                if (lane == 0) report(p.st, DEV_TIMEOUT);
+            }
+            if (lane == 0 && s_abort) {  // leave no product in flight
+                umma_commit(bar(S::B_DRAIN));
+                mbar_wait(bar(S::B_DRAIN), 0, ~0ull, p.st);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CK_REGS_ROWS));
+        // ------------------------------------------------------------ rows: thread (w, r) owns one
+        const int w = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + S::TM_S + w * 128, to = tmem + lanes + S::TM_O + w * D;
+        uint32_t s_phase = 0, h_phase = 0;  // completions of this tile's B_S, B_HALF
+        bool ok = true;
+        for (uint32_t kp = 0; ok; ++kp) {
+            const int at = take(kp);
+            if (at < 0) break;
+            int nt, key0, last;     // key tiles; the first key; the last key that the row sees
+            float m = -INFINITY;    // the row's reference, in the scores' units
+            {
+                const ChunkPiece pc = c.pieces[at];
+                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const int rows = ck_rows(sq, G, pc.t), row = pc.t * CK_ROWS + w * CK_M + r, tok = row / G;
+                nt = pc.kv1 - pc.kv0;
+                if (nt <= 0 || (w == 1 && rows <= CK_M)) continue;
+                const bool real = w * CK_M + r < rows;
+                key0 = pc.kv0 * CK_KT;
+                last = sq.len - sq.nq + tok;
+                if (!real) { last = 0x7fffffff; m = 0.f; }  // no row: nothing to mask, a reference that never moves
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.q + (real ? (sq.q0 + tok) * p.q_ts + (long long)(pc.h * G + row % G) * D : 0));
+                uint4 x[D / 8];  // its query, to the swizzled tile
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) x[k] = real ? src[k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -458,113 +711,125 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     *reinterpret_cast<uint4 *>(sm + w * CK_M * D * 2 + kmaj<128, 2>(r, k * 8, CK_M)) = x[k];
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive1(S::B_Q);
+                if (lane == 0) arrive1(S::B_Q + w);
             }
-            const int last = real ? first_new + tok : -1;            // the last key that the row sees
-            float m = -INFINITY, l = 0.f;                            // m in the scores' units
+            // the first step that some row of the warp does not see whole
+            const int mask_from = __reduce_min_sync(0xffffffffu, last < key0 ? 0 : (last - key0 + 1) / CK_STEP);
+            bool unset = true;  // some row has no reference yet
+            float l = 0.f;
             const float sc = p.scale_log2;
-            const uint32_t ts = tmem + lanes + S::TM_S + w * 128, to = tmem + lanes + S::TM_O + w * D;
-            if (w < act) {
-                for (int i = 0; i < nt; ++i) {
-                    if (!(ok = wait_warp(S::B_S + w, (s_phase + i) & 1))) break;
+            for (int j = 0; j < 2 * nt; ++j) {
+                const int h = j & 1;
+                if (h == 0) {
+                    if (!(ok = wait_warp(S::B_S + w, (s_phase + (j >> 1)) & 1))) break;
                     tc_fence_after();
-                    uint32_t x[128];
-                    tm_ld32(ts, x);
-                    tm_ld32(ts + 32, x + 32);
-                    tm_ld32(ts + 64, x + 64);
-                    tm_ld32(ts + 96, x + 96);
+                }
+                // both halves' weights lie over the first half's scores, which are read by then
+                const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
+                // Unmasked keys: the weights with the reference there is, looked at afterwards, so that no
+                // maximum stands between scores and weights.  A sum of the 64 up to 2^7 keeps every weight
+                // there too; past it the step is done again below, from the scores still in TMEM.
+                bool done = false;
+                float sum;
+                if (j < mask_from && !unset) {
+                    uint32_t x[CK_STEP], y[CK_STEP / 2];
+                    tm_ld32(sb, x);
+                    tm_ld32(sb + 32, x + 32);
                     tmem_wait_ld();
-                    const int lim = last - (pc.kv0 + i) * CK_KT;     // columns 0 .. lim are seen
-                    if (__any_sync(0xffffffffu, lim < CK_KT - 1)) {
+                    sum = ck_weights<BF, true>(x, y, sc, m * sc);
+                    done = !__any_sync(0xffffffffu, sum > 128.f);
+                    if (done) tm_st32(pb, y);
+                }
+                if (!done) {
+                    uint32_t x[CK_STEP], y[CK_STEP / 2];
+                    tm_ld32(sb, x);
+                    tm_ld32(sb + 32, x + 32);
+                    tmem_wait_ld();
+                    const int lim = last - key0 - j * CK_STEP;  // columns 0 .. lim are seen
+                    float mx = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < 128; ++k)
-                            if (k > lim) x[k] = 0xff800000u;
+                    for (int k = 0; k < CK_STEP; ++k) {
+                        if (k > lim) x[k] = 0xff800000u;
+                        mx = fmaxf(mx, __uint_as_float(x[k]));
                     }
-                    float m4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x[k]));
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    // a new reference where the row has none yet or its maximum outgrew it
-                    const bool grow = mx > -INFINITY && (m == -INFINITY || (mx - m) * sc > 8.f);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float f = grow ? ex2((m - mx) * sc) : 1.f;  // 2^-inf = 0 at first
-                        if (grow) m = mx;
+                    // the row's first reference, or its next one where a weight would pass 2
+                    const bool move = mx > -INFINITY && (m == -INFINITY || (mx - m) * sc > 1.f);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float f = move ? ex2((m - mx) * sc) : 1.f;  // 2^-inf = 0 at first
+                        if (move) m = mx;
                         l *= f;
-                        if (i > 0) {  // the products into O so far are done: B_S completed after them
-#pragma unroll
-                            for (int k = 0; k < D; k += 32) {
-                                uint32_t y[32];
-                                tm_ld32(to + k, y);
+                        if (j > 0) {  // the products of earlier tiles are done, those of this one's first half have to be
+                            if (h == 1) {
+                                if (!(ok = wait_warp(S::B_HALF + w, (h_phase + (j >> 1)) & 1))) break;
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int k = 0; k < D; k += 16) {
+                                float o[16];
+                                uint32_t z[16];
+                                tmem_ld16(to + k, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                                tm_st32(to + k, y);
+                                for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(o[e] * f);
+                                tm_st16(to + k, z);
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * sc;
-                    float l4[4] = {};
-#pragma unroll
-                    for (int k0 = 0; k0 < 128; k0 += 64) {
-                        uint32_t y[32];
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2) {
-                            const float a = ex2(fmaf(__uint_as_float(x[k0 + k]), sc, -ref));
-                            const float b = ex2(fmaf(__uint_as_float(x[k0 + k + 1]), sc, -ref));
-                            l4[k & 2] += a;
-                            l4[(k & 2) + 1] += b;
-                            y[k / 2] = pack16x2<BF>(a, b);
-                        }
-                        tm_st32(ts + k0 / 2, y);
-                    }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    tm_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive1(S::B_P + w);
+                    if (unset) unset = __any_sync(0xffffffffu, m == -INFINITY);
+                    sum = ck_weights<BF, false>(x, y, sc, m == -INFINITY ? 0.f : m * sc);
+                    tm_st32(pb, y);
                 }
-                // the sums, after the last product
-                if (ok && (ok = wait_warp(S::B_S + w, (s_phase + nt) & 1))) {
-                    tc_fence_after();
-                    const bool whole = pc.part_row < 0;
-                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: 0
-                    uint16_t *dst = p.out + ((long long)(sq.q0 + tok) * p.Hq + head) * D;
-                    float *part = p.part_o + ((long long)pc.part_row + row) * D;
-#pragma unroll
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t y[32];
-                        tm_ld32(to + k, y);
-                        tmem_wait_ld();
-                        if (!real) continue;
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 z;
-                                z.x = pack16x2<BF>(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv);
-                                z.y = pack16x2<BF>(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv);
-                                z.z = pack16x2<BF>(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv);
-                                z.w = pack16x2<BF>(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv);
-                                *reinterpret_cast<uint4 *>(dst + k + e) = z;
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(part + k + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                        }
-                    }
-                    if (real) {
-                        if (!whole) p.part_ml[pc.part_row + row] = make_float2(m == -INFINITY ? m : m * sc, l);
-                        else if (p.lse != nullptr)
-                            p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = m == -INFINITY ? -INFINITY : m * sc * LN2 + logf(l);
-                    }
-                    tc_fence_before();
-                }
-                s_phase += nt + 1;
+                l += sum;
+                tm_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive1(S::B_P + w * 2 + h);  // the products may begin on the first half
             }
+            // the sums, after the last product
+            if (ok && (ok = wait_warp(S::B_S + w, (s_phase + nt) & 1))) {
+                tc_fence_after();
+                const ChunkPiece pc = c.pieces[at];  // read again_%=: the loop above needs the registers
+                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const int row = w * CK_M + r, tok = (pc.t * CK_ROWS + row) / G, head = pc.h * G + (pc.t * CK_ROWS + row) % G;
+                const bool real = row < ck_rows(sq, G, pc.t);
+                const bool whole = pc.part_row < 0;
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: 0
+                uint16_t *dst = p.out + ((long long)(sq.q0 + tok) * p.Hq + head) * D;
+                float *part = p.part_o + ((long long)pc.part_row + row) * D;
+#pragma unroll
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t y[32];
+                    tm_ld32(to + k, y);
+                    tmem_wait_ld();
+                    if (!real) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 z;
+                            z.x = pack16x2<BF>(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv);
+                            z.y = pack16x2<BF>(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv);
+                            z.z = pack16x2<BF>(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv);
+                            z.w = pack16x2<BF>(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv);
+                            *reinterpret_cast<uint4 *>(dst + k + e) = z;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(part + k + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                }
+                if (real) {
+                    if (!whole) p.part_ml[pc.part_row + row] = make_float2(m == -INFINITY ? m : m * sc, l);
+                    else if (p.lse != nullptr)
+                        p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = m == -INFINITY ? -INFINITY : m * sc * LN2 + logf(l);
+                }
+                tc_fence_before();
+            }
+            s_phase += nt + 1;
+            h_phase += nt;
         }
-        if (nt > 0) ++done;
-        __syncthreads();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -624,7 +889,7 @@ static cudaError_t launch_chunk_t(const CUtensorMap &tk, const CUtensorMap &tv, 
     return cudaGetLastError();
 }
 
-// ws: the plan's part of the workspace: head (256 bytes), base [N], pieces.
+// ws: the plan's part of the workspace: head (256 bytes), base [N] (8 bytes each), pieces.
 cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void *ws, int d, bool bf, int sms, cudaStream_t stream) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     if (host_encoder(&enc) != 0) return cudaErrorUnknown;
@@ -635,8 +900,8 @@ cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void 
     ChunkParams c;
     c.p = p;
     c.head = static_cast<ChunkPlanHead *>(ws);
-    c.base = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + 256);
-    c.pieces = reinterpret_cast<ChunkPiece *>(reinterpret_cast<uint8_t *>(c.base) + ((size_t)p.N * 4 + 255) / 256 * 256);
+    c.base = reinterpret_cast<int2 *>(static_cast<uint8_t *>(ws) + 256);
+    c.pieces = reinterpret_cast<ChunkPiece *>(reinterpret_cast<uint8_t *>(c.base) + ((size_t)p.N * 8 + 255) / 256 * 256);
     c.max_pieces = m.pieces;
     c.max_entries = m.entries;
     c.max_rows = m.rows;
