@@ -44,6 +44,7 @@ constexpr int CK_REGS_ROWS = 216, CK_REGS_REST = 72;         // 256 x 216 + 128 
 struct ChunkPiece {
     int n, h, t, kv0, kv1;
     int part_row;
+    PagedSeq s;  // the sequence's numbers, checked
     int pad[2];
 };
 struct ChunkPlanHead {
@@ -90,12 +91,13 @@ constexpr int CK_CAND = 16;
 __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64, 128, 256};
 
 __device__ void ck_plan(const ChunkParams &c, int d) {
-    __shared__ unsigned long long s_w, s_wa, s_pieces[2][CK_CAND], s_rows[2][CK_CAND];
-    __shared__ int s_max, s_items, s_a, s_step, s_phi, s_entries, s_part, s_sum[2][33];
+    __shared__ unsigned long long s_w;
+    __shared__ unsigned s_wa, s_a, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // pieces and eighths of rows of one key head
+    __shared__ int s_max, s_items, s_step, s_phi, s_entries, s_part, s_sum[2][33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
-    if (tid == 0) { s_w = s_wa = 0; s_max = 1; s_items = s_a = s_entries = s_part = 0; }
-    if (tid < 2 * CK_CAND) s_pieces[tid / CK_CAND][tid % CK_CAND] = s_rows[tid / CK_CAND][tid % CK_CAND] = 0;
+    if (tid == 0) { s_w = 0; s_wa = s_a = 0; s_max = 1; s_items = s_entries = s_part = 0; }
+    if (tid < 2 * CK_CAND) s_pieces[tid] = s_rows8[tid] = 0;
     __syncthreads();
     // a warp a sequence, a lane a row tile
     unsigned long long w = 0;
@@ -128,45 +130,25 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     const float phi1 = (float)(all / c.sms * c.sms) / fmaxf((float)all, 1.f);
     // whole tiles of a sequence: ranks below, counted from the one with the most keys
     auto whole = [&](int tiles, int phi) { return phi ? (int)(tiles * phi1) : 0; };
-    int pieces[2][CK_CAND] = {};
-    unsigned rows[2][CK_CAND] = {};  // of one head; 2^32 of them would take 2 TB
-    unsigned long long wa = 0;
-    int na = 0;
-    float inv[CK_CAND];
-#pragma unroll
-    for (int j = 0; j < CK_CAND; ++j) inv[j] = 1.f / ((s_max + ck_div[j] - 1) / ck_div[j]);
-    for (int n = warp; n < p.N; n += warps) {
-        const PagedSeq s = paged_seq(p, n, false);
-        const int tiles = ck_tiles(s, G);
-        for (int t = lane; t < tiles; t += 32) {
-            const int k = ck_keys(s, G, t), r = ck_rows(s, G, t);
-            const bool a = tiles - 1 - t < whole(tiles, 1);
-            if (a) { wa += k; ++na; }
-#pragma unroll
-            for (int j = 0; j < CK_CAND; ++j) {
-                const int ns = (int)ceilf(k * inv[j] - 1e-3f);  // near enough for the choice
-                pieces[0][j] += ns;
-                if (ns > 1) rows[0][j] += (unsigned)ns * r;
-                if (!a) {
-                    pieces[1][j] += ns;
-                    if (ns > 1) rows[1][j] += (unsigned)ns * r;
+    {   // a lane a candidate; few sequences share the warps among their tiles
+        const int q = lane / CK_CAND, split = max(1, warps / p.N);
+        const float inv = 1.f / ((s_max + ck_div[lane % CK_CAND] - 1) / ck_div[lane % CK_CAND]);
+        unsigned pieces = 0, rows8 = 0, wa = 0, na = 0;
+        for (int v = warp; v < p.N * split; v += warps) {
+            const PagedSeq s = paged_seq(p, v % p.N, false);
+            const int tiles = ck_tiles(s, G), a = whole(tiles, 1);
+            for (int t = v / p.N; t < tiles; t += split) {
+                const int k = ck_keys(s, G, t), ns = (int)ceilf(k * inv - 1e-3f);  // near enough for the choice
+                const bool in_a = tiles - 1 - t < a;
+                if (in_a) { wa += k; ++na; }
+                if (!(q && in_a)) {
+                    pieces += ns;
+                    if (ns > 1) rows8 += ns * ((ck_rows(s, G, t) + 7) / 8);
                 }
             }
         }
-    }
-    if (items) {  // the same in every lane
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < CK_CAND; ++j) {
-                const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)pieces[q][j]), b = __reduce_add_sync(0xffffffffu, rows[q][j]);
-                if (lane == 0) {
-                    atomicAdd(&s_pieces[q][j], (unsigned long long)a);
-                    atomicAdd(&s_rows[q][j], (unsigned long long)b);
-                }
-            }
-        wa = warp_sum(wa);
-        na = __reduce_add_sync(0xffffffffu, na);
+        atomicAdd(&s_pieces[lane], pieces);
+        atomicAdd(&s_rows8[lane], rows8);
         if (lane == 0) {
             atomicAdd(&s_wa, wa);
             atomicAdd(&s_a, na);
@@ -175,9 +157,9 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     __syncthreads();
     if (warp == 0) {
         const int q = lane / CK_CAND, j = lane % CK_CAND, step = (s_max + ck_div[j] - 1) / ck_div[j];
-        const float S = (float)c.sms, R = (float)s_rows[q][j] * p.Hkv;
+        const float S = (float)c.sms, R = (float)s_rows8[lane] * 8.f * p.Hkv;
         const float pa = q ? (float)s_a * p.Hkv : 0.f, ta = q && s_a ? (float)s_wa / s_a + 3.f : 0.f;
-        const float pb = (float)s_pieces[q][j] * p.Hkv, tb = pb > 0.f ? (float)(s_w - (q ? s_wa : 0)) * p.Hkv / pb + 3.f : 3.f;
+        const float pb = (float)s_pieces[lane] * p.Hkv, tb = pb > 0.f ? (float)(s_w - (q ? s_wa : 0)) * p.Hkv / pb + 3.f : 3.f;
         const float ka = ceilf(pa / S), early = (ka * S - pa) * floorf(ta / tb);
         float cost = ka * ta + (pb > early ? fmaxf(ceilf((pb - early) / S) * tb, fminf(step + 3.f, tb * 2.f)) : 0.f);
         if (R > 0.f) cost += 3.f + R * d * 8.f * 1.2e-7f;
@@ -263,7 +245,7 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
                         const int row = part < 0 ? -1 : part + j * r;
                         // a piece without room for its sums is left empty
                         const bool room = part < 0 || part + ns * r <= c.max_rows;
-                        c.pieces[i + j] = {n, h, t, j * st, room ? min(k, (j + 1) * st) : j * st, row, {0, 0}};
+                        c.pieces[i + j] = {n, h, t, j * st, room ? min(k, (j + 1) * st) : j * st, row, s, {0, 0}};
                     }
                 }
             }
@@ -595,7 +577,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 at = __shfl_sync(0xffffffffu, at, 0);
                 if (at < 0) break;
                 const ChunkPiece pc = c.pieces[at];
-                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const PagedSeq sq = pc.s;
                 const int kv_end = paged_kv_end(sq, G, (pc.t + 1) * CK_ROWS - 1);
                 const int *trow = p.table + (long long)sq.row * p.P;
                 const int box = min(p.page_size, CK_KT);  // tokens of one copy
@@ -662,7 +644,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int at = take(k);
                 if (at < 0) break;
                 const ChunkPiece pc = c.pieces[at];
-                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const PagedSeq sq = pc.s;
                 const int nt = pc.kv1 - pc.kv0;
                 if (nt <= 0) continue;
                 if (elect_lane()) ok = is.run(nt, ck_rows(sq, G, pc.t) > CK_M);
@@ -691,12 +673,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (at < 0) break;
             int nt, key0, last;     // key tiles; the first key; the last key that the row sees
             float m = -INFINITY;    // the row's reference, in the scores' units
+            bool idle;              // the warp has no row: what its lanes of TMEM hold goes nowhere
             {
                 const ChunkPiece pc = c.pieces[at];
-                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const PagedSeq sq = pc.s;
                 const int rows = ck_rows(sq, G, pc.t), row = pc.t * CK_ROWS + w * CK_M + r, tok = row / G;
                 nt = pc.kv1 - pc.kv0;
                 if (nt <= 0 || (w == 1 && rows <= CK_M)) continue;
+                idle = w * CK_M + (warp & 3) * 32 >= rows;
                 const bool real = w * CK_M + r < rows;
                 key0 = pc.kv0 * CK_KT;
                 last = sq.len - sq.nq + tok;
@@ -723,6 +707,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (h == 0) {
                     if (!(ok = wait_warp(S::B_S + w, (s_phase + (j >> 1)) & 1))) break;
                     tc_fence_after();
+                }
+                if (idle) {
+                    __syncwarp();
+                    if (lane == 0) arrive1(S::B_P + w * 2 + h);
+                    continue;
                 }
                 // both halves' weights lie over the first half's scores, which are read by then
                 const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
@@ -789,7 +778,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (ok && (ok = wait_warp(S::B_S + w, (s_phase + nt) & 1))) {
                 tc_fence_after();
                 const ChunkPiece pc = c.pieces[at];  // read again_%=: the loop above needs the registers
-                const PagedSeq sq = paged_seq(p, pc.n, false);
+                const PagedSeq sq = pc.s;
                 const int row = w * CK_M + r, tok = (pc.t * CK_ROWS + row) / G, head = pc.h * G + (pc.t * CK_ROWS + row) % G;
                 const bool real = row < ck_rows(sq, G, pc.t);
                 const bool whole = pc.part_row < 0;
