@@ -449,7 +449,7 @@ static cudaError_t launch_join_t(const PagedParams &p, const int *count, int max
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int groups = tile_rows > 64 ? 4 : 2;  // blocks of eight warps over an item's rows
+    const int groups = tile_rows > 64 ? 8 : 2;  // blocks of eight warps over an item's rows
     cfg.gridDim = dim3(max_entries < 2 * sms ? max_entries : 2 * sms, groups);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;

@@ -697,6 +697,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 __syncwarp();
                 if (lane == 0) arrive1(S::B_Q + w);
             }
+            if (idle) {  // the products' turns, and nothing else
+                for (int i = 0; i < nt && (ok = wait_warp(S::B_S + w, (s_phase + i) & 1)); ++i)
+                    if (lane < 2) arrive1(S::B_P + w * 2 + lane);
+                ok = ok && wait_warp(S::B_S + w, (s_phase + nt) & 1);
+                s_phase += nt + 1;
+                h_phase += nt;
+                continue;
+            }
             // the first step that some row of the warp does not see whole
             const int mask_from = __reduce_min_sync(0xffffffffu, last < key0 ? 0 : (last - key0 + 1) / CK_STEP);
             bool unset = true;  // some row has no reference yet
@@ -707,11 +715,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (h == 0) {
                     if (!(ok = wait_warp(S::B_S + w, (s_phase + (j >> 1)) & 1))) break;
                     tc_fence_after();
-                }
-                if (idle) {
-                    __syncwarp();
-                    if (lane == 0) arrive1(S::B_P + w * 2 + h);
-                    continue;
                 }
                 // both halves' weights lie over the first half's scores, which are read by then
                 const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
