@@ -20,7 +20,7 @@ bool paged_chunk_pages(int page_size);
 ChunkLimits paged_chunk_limits(int N, int total_q, int G, int Hkv, int span, int sms);
 size_t paged_chunk_piece_bytes();
 cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void *ws, int d, bool bf, int sms, cudaStream_t stream);
-cudaError_t launch_pages_free(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream);
 int compact_blocks(int num_pages);
 cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t stream);
@@ -290,7 +290,7 @@ int kda_pages_free(int *table, int *length, int *ref, const int *rows, int n, in
     if (device_status(&p.st) != KDA_OK) return KDA_ERR_CUDA;
     p.rows = rows;
     p.n = n;
-    return to_status(kda::launch_pages_free(p, static_cast<cudaStream_t>(stream)));
+    return to_status(kda::launch_pages_free(p, kda::host_num_sms(device()), static_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_pages_compact_workspace_bytes(int num_pages) {

@@ -287,6 +287,7 @@ __device__ void ck_append(const ChunkParams &c, long long first, long long step)
 
 template <int D>
 __global__ void __launch_bounds__(512) paged_plan_kernel(const ChunkParams c) {
+    launch_dependents();  // the chunk kernel sets itself up meanwhile
     if (blockIdx.x == 0) ck_plan(c, D);
     else ck_append<D>(c, (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x, (long long)(gridDim.x - 1) * blockDim.x);
 }
@@ -531,6 +532,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)words[3];
+    wait_for_primary();  // the plan, and the new tokens in their pages
+    asm volatile("fence.proxy.async;" ::: "memory");  // which the tensor copies read
     const int pieces = c.head->pieces;
     auto wait1 = [&](int i, uint32_t par) -> bool {
         if (ck_wait(bar(i), par, tries)) return true;
@@ -877,8 +880,17 @@ static cudaError_t launch_chunk_t(const CUtensorMap &tk, const CUtensorMap &tv, 
     const int more = c.p.k_new == nullptr ? 0 : (int)(blocks < 2LL * c.sms ? blocks : 2LL * c.sms);
     paged_plan_kernel<D><<<1 + more, 512, 0, stream>>>(c);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    paged_chunk_kernel<D, BF><<<c.max_pieces < c.sms ? c.max_pieces : c.sms, CK_THREADS, CkShape<D>::SMEM, stream>>>(tk, tv, c);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c.max_pieces < c.sms ? c.max_pieces : c.sms);
+    cfg.blockDim = dim3(CK_THREADS);
+    cfg.dynamicSmemBytes = CkShape<D>::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, BF>, tk, tv, c);
 }
 
 // ws: the plan's part of the workspace: head (256 bytes), base [N] (8 bytes each), pieces.

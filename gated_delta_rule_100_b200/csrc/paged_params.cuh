@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "kda_device.cuh"
+#include "launch_order.cuh"
 
 namespace kda {
 
@@ -89,9 +90,5 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float LN2 = 0.69314718055994531f;
-
-// Launch-order hints between a kernel and the one after it on the stream.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace kda

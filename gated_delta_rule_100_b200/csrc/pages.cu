@@ -13,6 +13,7 @@
 // reported; so is a reservation for which there are too few pages, through its
 // info word.
 #include <cooperative_groups.h>
+#include <stddef.h>
 
 #include "pages_params.cuh"
 
@@ -67,9 +68,11 @@ __device__ __forceinline__ bool mark_rows(const int *rows, int n, int R, uint32_
 
 // ------------------------------------------------------------------- free ----
 // Every block checks the whole list (a few reads a thread), then takes rows in
-// turn, a warp a row.
+// turn: 256 entries at a time, so a row of 750 pages costs three round trips to
+// the counts (a warp a row took 24: 15.7 us for 200 rows, from 7).
 __global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
     __shared__ uint32_t bits[PG_MAX_ROWS / 32];
+    wait_for_primary();
     for (int i = threadIdx.x; i < (p.R + 31) / 32; i += blockDim.x) bits[i] = 0;
     __syncthreads();
     const bool ok = mark_rows(p.rows, p.n, p.R, bits);
@@ -77,13 +80,11 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
         if (threadIdx.x == 0) report(p.st, DEV_BAD_ARG);
         return;
     }
-    const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
-    for (int i = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); i < p.n; i += warps) {
+    for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int row = p.rows[i];
         int *tr = p.table + (long long)row * p.P;
-        const int len = p.length[row];
-        const int held = min(pages_of(max(len, 0), p.ps), p.P);
-        for (int j = lane; j < held; j += 32) {
+        const int held = min(pages_of(max(p.length[row], 0), p.ps), p.P);
+        for (int j = threadIdx.x; j < held; j += blockDim.x) {
             const int page = tr[j];
             tr[j] = -1;
             if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
                 report(p.st, DEV_BAD_ARG);
             }
         }
-        __syncwarp();
-        if (lane == 0) p.length[row] = 0;
+        __syncthreads();  // every thread has read the length
+        if (threadIdx.x == 0) p.length[row] = 0;
     }
 }
 
@@ -106,10 +107,15 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
 struct GrantShared {
     int sm[33];
     uint32_t bits[PG_MAX_ROWS / 32];
-    int start[PG_MAX_LIST + 1];  // exclusive prefix of the sequences' needs
     int warp_free[PG_WARPS];
     int cta_free;
+    int found[PG_WARPS][128];    // a step's free pages, in order
+    int start[PG_MAX_LIST + 1];  // exclusive prefix of the sequences' needs
+    int row[PG_MAX_LIST];        // their rows
+    int held[PG_MAX_LIST];       // entries that the rows hold before (a fork's: full pages of the source)
 };
+// what of it a list of n needs
+__host__ __device__ constexpr size_t grant_bytes(int n) { return offsetof(GrantShared, start) + sizeof(int) * (3 * (size_t)n + 1); }
 
 // Free flags of pages [4 i, 4 i + 4).
 __device__ __forceinline__ uint32_t free_nibble(const int *ref, int num_pages, int i) {
@@ -126,10 +132,13 @@ __device__ __forceinline__ uint32_t free_nibble(const int *ref, int num_pages, i
 
 template <bool FORK>
 __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS) pages_grant_kernel(const PagesParams p) {
-    __shared__ GrantShared s;
+    extern __shared__ __align__(16) uint8_t raw[];
+    GrantShared &s = *reinterpret_cast<GrantShared *>(raw);
+    int *s_start = s.start, *s_row = s.start + p.n + 1, *s_held = s_row + p.n;  // packed for n
     cg::cluster_group cluster = cg::this_cluster();
     const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    wait_for_primary();
     // ---- the list: rows in range and named once; what each needs
     for (int i = tid; i < (p.R + 31) / 32; i += PG_THREADS) s.bits[i] = 0;
     __syncthreads();
@@ -138,9 +147,10 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     int total = 0;
     for (int base = 0; base < p.n; base += PG_THREADS) {
         const int i = base + tid;
-        int need = 0;
+        int need = 0, held = 0;
         if (i < p.n) {
             const int row = p.rows[i];
+            s_row[i] = row;
             if (row >= 0 && row < p.R) {
                 const int have = p.length[row];
                 if constexpr (FORK) {
@@ -150,21 +160,21 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
                     } else {
                         const int len = p.length[from];
                         if (len < 0 || pages_of(len, p.ps) > p.P) ok = false;
-                        else need = len % p.ps != 0;
+                        else { need = len % p.ps != 0; held = len / p.ps; }
                     }
                 } else {
                     const int want = p.new_length[i];
                     if (have < 0 || want < have || pages_of(want, p.ps) > p.P) ok = false;
-                    else need = pages_of(want, p.ps) - pages_of(have, p.ps);
+                    else { held = pages_of(have, p.ps); need = pages_of(want, p.ps) - held; }
                 }
             }
         }
         int sum;
         const int at = block_prefix(need, s.sm, sum);
-        if (i < p.n) s.start[i] = total + at;
+        if (i < p.n) { s_start[i] = total + at; s_held[i] = held; }
         total += sum;  // at most the table's entries, which the host holds below 2^31
     }
-    if (tid == 0) s.start[p.n] = total;
+    if (tid == 0) s_start[p.n] = total;
     auto no_copies = [&]() {
         if constexpr (FORK)
             for (int i = cta * PG_THREADS + tid; i < p.n; i += PG_CLUSTER * PG_THREADS) p.copy_src[i] = p.copy_dst[i] = -1;
@@ -210,7 +220,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
         return;
     }
 
-    // ---- the free pages of ranks below `total` go to their sequences
+    // ---- the free pages of ranks below `total` go to their sequences: a step's are listed, then a lane takes one
     for (int k = s0; k < s1 && rank < total; ++k) {
         const uint32_t m = free_nibble(p.ref, p.num_pages, k * 32 + lane);
         const int c = __popc(m);
@@ -220,48 +230,45 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        int f = rank + incl - c;
-        for (int b = 0; b < 4; ++b) {
-            if (!(m >> b & 1u)) continue;
-            if (f < total) {
-                int lo = 0, hi = p.n - 1;  // the last sequence with start <= f
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) / 2;
-                    if (s.start[mid] <= f) lo = mid; else hi = mid - 1;
-                }
-                const int row = p.rows[lo], page = (k * 32 + lane) * 4 + b;
-                if constexpr (FORK) {
-                    const int full = p.length[p.src[lo]] / p.ps;  // a source's length does not change here
-                    p.copy_src[lo] = p.table[(long long)p.src[lo] * p.P + full];
-                    p.copy_dst[lo] = page;
-                    p.table[(long long)row * p.P + full] = page;
-                } else {
-                    // this row's first new entry follows those that its old length holds
-                    const int held = pages_of(p.new_length[lo], p.ps) - (s.start[lo + 1] - s.start[lo]);
-                    p.table[(long long)row * p.P + held + f - s.start[lo]] = page;
-                }
-                p.ref[page] = 1;
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
+        for (int b = 0, at = incl - c; b < 4; ++b)
+            if (m >> b & 1u) s.found[warp][at++] = (k * 32 + lane) * 4 + b;
+        __syncwarp();
+        for (int q = lane; q < all && rank + q < total; q += 32) {
+            const int f = rank + q, page = s.found[warp][q];
+            int lo = 0, hi = p.n - 1;  // the last sequence with start <= f
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_start[mid] <= f) lo = mid; else hi = mid - 1;
             }
-            ++f;
+            // its entries so far come first
+            p.table[(long long)s_row[lo] * p.P + s_held[lo] + f - s_start[lo]] = page;
+            p.ref[page] = 1;
+            if constexpr (FORK) {
+                p.copy_src[lo] = p.table[(long long)p.src[lo] * p.P + s_held[lo]];
+                p.copy_dst[lo] = page;
+            }
         }
-        rank += __shfl_sync(0xffffffffu, incl, 31);
+        rank += all;
+        __syncwarp();
     }
     if constexpr (!FORK) {
         for (int i = cta * PG_THREADS + tid; i < p.n; i += PG_CLUSTER * PG_THREADS) p.length[p.rows[i]] = p.new_length[i];
     } else {
-        // the full pages, shared: a warp a branch
-        for (int i = gw; i < p.n; i += warps) {
-            const int from = p.src[i], row = p.rows[i], len = p.length[from], full = len / p.ps;
-            const int *a = p.table + (long long)from * p.P;
-            int *b = p.table + (long long)row * p.P;
-            for (int j = lane; j < full; j += 32) {
+        // the full pages, shared: the warps share out the branches
+        const int each = max(1, warps / max(1, p.n));  // warps of a branch
+        for (int v = gw; v < p.n * each; v += warps) {
+            const int i = v / each, sub = v % each, full = s_held[i], len = p.length[p.src[i]];
+            const int *a = p.table + (long long)p.src[i] * p.P;
+            int *b = p.table + (long long)s_row[i] * p.P;
+            for (int j = sub * 32 + lane; j < full; j += each * 32) {
                 const int page = a[j];
                 b[j] = page;
                 if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
                 else report(p.st, DEV_BAD_ARG);
             }
-            if (lane == 0) {
-                p.length[row] = len;
+            if (lane == 0 && sub == 0) {
+                p.length[s_row[i]] = len;
                 if (len % p.ps == 0) p.copy_src[i] = p.copy_dst[i] = -1;
             }
         }
@@ -277,6 +284,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
 constexpr int CP_BLOCK = 4096, CP_THREADS = 1024;
 
 __global__ void __launch_bounds__(CP_THREADS) compact_count_kernel(const PagesParams p) {
+    wait_for_primary();
     const int i = blockIdx.x * CP_THREADS + threadIdx.x;
     const int dead = __popc(free_nibble(p.ref, p.num_pages, i));
     const int in = min(4, max(0, p.num_pages - 4 * i));
@@ -289,6 +297,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_count_kernel(const PagesPa
 __global__ void __launch_bounds__(CP_THREADS) compact_rank_kernel(const PagesParams p, int blocks) {
     __shared__ int sm[33];
     const int tid = threadIdx.x;
+    wait_for_primary();
     // live pages in all, before this block, and in the blocks before the one that page n lies in
     int mine = 0, before = 0;
     for (int b = tid; b < blocks; b += CP_THREADS) {
@@ -327,6 +336,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_rank_kernel(const PagesPar
 }
 
 __global__ void __launch_bounds__(256) compact_apply_kernel(const PagesParams p) {
+    wait_for_primary();
     const int n = p.ws_n[0], moves = p.ws_n[1];
     const long long all = (long long)gridDim.x * blockDim.x, me = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     for (long long i = me; i < p.num_pages; i += all) {
@@ -367,6 +377,7 @@ constexpr int COPY_THREADS = 256, COPY_UNIT = 16384;
 
 template <bool CHECK>
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolParams p) {
+    wait_for_primary();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
     const long long per_page = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT, per_pair = per_page * p.outer;
     const long long units = n * per_pair;
@@ -410,32 +421,50 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolPara
 }
 
 // ------------------------------------------------------------------- host ----
-cudaError_t launch_pages_free(const PagesParams &p, cudaStream_t stream) {
-    const int grid = (p.n + 7) / 8;
-    pages_free_kernel<<<grid < 296 ? grid : 296, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+// Every kernel here is launched so that its blocks may be in place when the one
+// before it ends (each waits for that end first): a fork's three launches on
+// small lists are mostly launches.
+template <class K, class... A>
+static cudaError_t launch_behind(K *kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_pages_free(const PagesParams &p, int sms, cudaStream_t stream) {
+    return launch_behind(pages_free_kernel, dim3(p.n < 8 * sms ? p.n : 8 * sms), 256, 0, stream, p);
 }
 cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream) {
-    if (fork) pages_grant_kernel<true><<<PG_CLUSTER, PG_THREADS, 0, stream>>>(p);
-    else pages_grant_kernel<false><<<PG_CLUSTER, PG_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    auto *k = fork ? pages_grant_kernel<true> : pages_grant_kernel<false>;
+    const size_t smem = grant_bytes(p.n);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grant_bytes(PG_MAX_LIST));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_behind(k, dim3(PG_CLUSTER), PG_THREADS, smem, stream, p);
 }
 int compact_blocks(int num_pages) { return (num_pages + CP_BLOCK - 1) / CP_BLOCK; }
 cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t stream) {
     const int blocks = compact_blocks(p.num_pages);
-    compact_count_kernel<<<blocks, CP_THREADS, 0, stream>>>(p);
-    compact_rank_kernel<<<blocks, CP_THREADS, 0, stream>>>(p, blocks);
+    cudaError_t e = launch_behind(compact_count_kernel, dim3(blocks), CP_THREADS, 0, stream, p);
+    if (e == cudaSuccess) e = launch_behind(compact_rank_kernel, dim3(blocks), CP_THREADS, 0, stream, p, blocks);
+    if (e != cudaSuccess) return e;
     const long long want = ((long long)p.R * p.P + 255) / 256, want2 = (p.num_pages + 255) / 256, top = 8LL * sms;
     const long long grid = want > want2 ? want : want2;
-    compact_apply_kernel<<<(int)(grid < top ? grid : top), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_behind(compact_apply_kernel, dim3((unsigned)(grid < top ? grid : top)), 256, 0, stream, p);
 }
 cudaError_t launch_pages_copy(const PoolParams &p, bool check, int sms, cudaStream_t stream) {
     const long long units = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT * p.outer * p.n, top = 8LL * sms;
-    const int grid = (int)(units < top ? units : top);
-    if (check) pages_copy_kernel<true><<<grid, COPY_THREADS, 0, stream>>>(p);
-    else pages_copy_kernel<false><<<grid, COPY_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_behind(check ? pages_copy_kernel<true> : pages_copy_kernel<false>, dim3((unsigned)(units < top ? units : top)),
+                         COPY_THREADS, 0, stream, p);
 }
 
 }  // namespace kda

@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include "kda_device.cuh"
+#include "launch_order.cuh"
 
 namespace kda {
 
