@@ -12,7 +12,7 @@ namespace kda {
 int paged_rows_slots(int ctas);
 int paged_rows_ctas_per_sm(int d);
 int paged_rows_tile();
-cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, int ctas, cudaStream_t stream);
+cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, bool whole, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, const int *count, int max_entries, int tile_rows, int sms,
                               cudaStream_t stream);
 int paged_chunk_tile();
@@ -52,8 +52,11 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
 // few rows runs.
 constexpr int kFewRows = 16;
 
+// Keys of a full table up to which the kernel of few rows takes items whole.
+constexpr int kWholeKeys = 512;
+
 struct AttnPlan {
-    bool chunk;
+    bool chunk, whole;
     int ctas, entries, tile, sms;
     kda::ChunkLimits lim;
     size_t off_entries, off_ml, off_o, bytes;
@@ -78,14 +81,16 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
         const long long tiles = (long long)total_q * G / a.tile + seqs;
         const long long span = ((long long)P * page_size + 63) / 64;
         const long long top = (long long)a.sms * kda::paged_rows_ctas_per_sm(d);
+        a.whole = (long long)P * page_size <= kWholeKeys;
         a.ctas = (int)top;
-        if (tiles < top && tiles * Hkv < top && tiles * Hkv * span < top) a.ctas = (int)(tiles * Hkv * span);
-        a.entries = a.ctas;
-        rows = (long long)kda::paged_rows_slots(a.ctas) * a.tile;
+        if (a.whole) a.ctas = (int)(tiles * Hkv < top ? tiles * Hkv : top);
+        else if (tiles < top && tiles * Hkv < top && tiles * Hkv * span < top) a.ctas = (int)(tiles * Hkv * span);
+        a.entries = a.whole ? 0 : a.ctas;
+        rows = a.whole ? 0 : (long long)kda::paged_rows_slots(a.ctas) * a.tile;
     }
     a.off_ml = a.off_entries + up256((size_t)a.entries * sizeof(kda::SplitEntry));
     a.off_o = a.off_ml + up256((size_t)rows * sizeof(float2));
-    a.bytes = a.off_o + (size_t)rows * d * sizeof(float);
+    a.bytes = a.off_o + (size_t)rows * d * sizeof(float) + 16;
     return a;
 }
 
@@ -240,7 +245,8 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
         const int *count = reinterpret_cast<const int *>(ws) + 2;  // ChunkPlanHead::entries
         return to_status(kda::launch_paged_join(p, d, bf, count, pl.entries, pl.tile, pl.sms, s));
     }
-    if (kda::launch_paged_rows(p, d, bf, pl.ctas, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (kda::launch_paged_rows(p, d, bf, pl.whole, pl.ctas, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (pl.whole) return KDA_OK;
     return to_status(kda::launch_paged_join(p, d, bf, nullptr, pl.entries, pl.tile, pl.sms, s));
 }
 

@@ -38,8 +38,8 @@ struct PaShape {
     static constexpr int STAGE = 2 * TILE;                    // keys and values
     static constexpr int STAGES = D == 128 ? 3 : 4;
     static constexpr int RING = STAGE * STAGES;               // per warp
-    static constexpr int MERGE = PA_WARPS * PA_ROWS * D * 4;  // fp32 sums, reusing the rings
-    static constexpr int SMEM = PA_WARPS * RING > MERGE ? PA_WARPS * RING : MERGE;
+    static constexpr int MSTRIDE = D + 8;                     // floats of a row of sums (padded: eight rows at a time)
+    static constexpr int SMEM = PA_WARPS * RING + PA_ROWS * MSTRIDE * 4;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
@@ -76,14 +76,14 @@ __device__ __forceinline__ int pa_units(const PagedSeq &s, int G, int t) {
     return max(1, (paged_kv_end(s, G, (t + 1) * PA_ROWS - 1) + PA_UNIT - 1) / PA_UNIT);
 }
 __device__ __forceinline__ int pa_tiles(const PagedSeq &s, int G) { return (s.nq * G + PA_ROWS - 1) / PA_ROWS; }
-__device__ __forceinline__ long long pa_head_units(const PagedSeq &s, int G) {
-    long long w = 0;
-    const int tiles = pa_tiles(s, G);
-    for (int t = 0; t < tiles; ++t) w += pa_units(s, G, t);
-    return w;
-}
+// A run's part of one item.
+struct PaPiece {
+    PagedSeq s;
+    int n, h, t, off, cnt, units;
+};
 
-template <int D, bool BF>
+// WHOLE: an item is one unit of the plan, so nothing is split or joined (short caches).
+template <int D, bool BF, bool WHOLE>
 __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParams p) {
     using S = PaShape<D>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -95,14 +95,18 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.G, c = blockIdx.x, grid = gridDim.x;
     launch_dependents();
+    auto plan_units = [&](const PagedSeq &s, int t) { return WHOLE ? 1 : pa_units(s, G, t); };
+    auto head_units = [&](const PagedSeq &s) {
+        if (WHOLE) return (long long)pa_tiles(s, G);
+        long long w = 0;
+        for (int t = 0; t < pa_tiles(s, G); ++t) w += pa_units(s, G, t);
+        return w;
+    };
 
     // ---- plan: the units of every sequence, and the item that this run begins in
     const int per = (p.N + PA_THREADS - 1) / PA_THREADS;
     long long mine = 0;
-    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) {
-        const PagedSeq s = paged_seq(p, n, c == 0);
-        mine += pa_head_units(s, G) * p.Hkv;
-    }
+    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) mine += head_units(paged_seq(p, n, c == 0)) * p.Hkv;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
         W += s_sum[w];
     }
     const long long runs = W < grid ? W : grid;  // every run has at least one unit
-    if (tid == 0) p.entries[c].count = 0;
+    if (!WHOLE && tid == 0) p.entries[c].count = 0;
     if (c >= runs) return;
     long long u = c * W / runs;
     const long long u_end = (c + 1) * W / runs;
@@ -126,130 +130,138 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
         int n = tid * per;
         for (;; ++n) {
             const PagedSeq s = paged_seq(p, n, false);
-            const long long hu = pa_head_units(s, G), w = hu * p.Hkv;
+            const long long hu = head_units(s), w = hu * p.Hkv;
             if (left >= w) { left -= w; start += w; continue; }
             const int h = (int)(left / hu);
             left -= h * hu;
             start += h * hu;
             int t = 0;
-            for (int k; left >= (k = pa_units(s, G, t)); ++t) { left -= k; start += k; }
+            for (int k; left >= (k = plan_units(s, t)); ++t) { left -= k; start += k; }
             s_n = n; s_h = h; s_t = t; s_start = start;
             break;
         }
     }
     __syncthreads();
-    int n = s_n, h = s_h, t = s_t;
     long long start = s_start;                   // the item's first unit
 
     const uint32_t ring = smem_u32(smem) + warp * S::RING;
+    float *sums = reinterpret_cast<float *>(smem + PA_WARPS * S::RING);
     const int g8 = lane >> 2, t4 = lane & 3;
-    PagedSeq s = paged_seq(p, n, false);
 
-    while (u < u_end) {
-        const int units = pa_units(s, G, t);
-        const int off = (int)(u - start);
-        const int cnt = (int)min((long long)(units - off), u_end - u);
-        const int rows = s.nq * G;
-        const int kv_end = paged_kv_end(s, G, (t + 1) * PA_ROWS - 1);
-        const int first_new = s.len - s.nq;      // may be negative: tokens without a place
-        const int *trow = p.table + (long long)s.row * p.P;
-
-        // the new tokens' keys and values of this run go to their pages; they are
-        // read below from where they came, so nothing waits for these stores
-        if (p.k_new != nullptr && t == 0) {
-            // (row tile 0's last unit writes what no unit of it covers: a tile sees at least the first token)
-            const int lo = max(max(off * PA_UNIT, first_new), 0);
-            const int hi = off + cnt == units ? s.len : min(s.len, (off + cnt) * PA_UNIT);
-            constexpr int CH = D / 8;
-            for (int i = tid; i < max(hi - lo, 0) * CH; i += PA_THREADS) {
-                const int pos = lo + i / CH, ch = i % CH, tok = s.q0 + pos - first_new;
-                const int page = trow[pos / p.page_size], in = pos % p.page_size;
-                if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
-                const uint4 kx = *reinterpret_cast<const uint4 *>(p.k_new + tok * p.kn_ts + h * D + ch * 8);
-                const uint4 vx = *reinterpret_cast<const uint4 *>(p.v_new + tok * p.vn_ts + h * D + ch * 8);
-                *reinterpret_cast<uint4 *>(p.kp + page * p.k_ps + in * p.k_ts + h * p.k_hs + ch * 8) = kx;
-                *reinterpret_cast<uint4 *>(p.vp + page * p.v_ps + in * p.v_ts + h * p.v_hs + ch * 8) = vx;
-            }
-        }
-
-        // ---- the warp's loads: 16 keys of each unit
-        const uint16_t *kptr = p.kp, *vptr = p.vp;
-        bool kvalid = false;
-        auto locate = [&](int step) {  // lane l < 16: where key l of the step lies
-            const int pos = (off + step) * PA_UNIT + warp * PA_WKEYS + (lane & 15);
-            kvalid = step < cnt && pos < kv_end;
-            kptr = p.kp;
-            vptr = p.vp;
-            if (kvalid) {
-                if (p.k_new != nullptr && pos >= first_new) {
-                    const long long tok = s.q0 + pos - first_new;
-                    kptr = p.k_new + tok * p.kn_ts + h * D;
-                    vptr = p.v_new + tok * p.vn_ts + h * D;
+    // the run's part of the item at unit u, which begins at unit `start`
+    auto take = [&](PaPiece &pc) {
+        pc.units = pa_units(pc.s, G, pc.t);
+        pc.off = WHOLE ? 0 : (int)(u - start);
+        pc.cnt = WHOLE ? pc.units : (int)min((long long)(pc.units - pc.off), u_end - u);
+    };
+    // ---- the warp's loads: 16 keys of each unit
+    const uint16_t *kptr = p.kp, *vptr = p.vp;
+    bool kvalid = false;
+    auto locate = [&](const PaPiece &pc, int step) {  // lane l < 16: where key l of the step lies
+        const int pos = (pc.off + step) * PA_UNIT + warp * PA_WKEYS + (lane & 15), first_new = pc.s.len - pc.s.nq;
+        kvalid = step < pc.cnt && pos < paged_kv_end(pc.s, G, (pc.t + 1) * PA_ROWS - 1);
+        kptr = p.kp;
+        vptr = p.vp;
+        if (kvalid) {
+            if (p.k_new != nullptr && pos >= first_new) {
+                const long long tok = pc.s.q0 + pos - first_new;
+                kptr = p.k_new + tok * p.kn_ts + pc.h * D;
+                vptr = p.v_new + tok * p.vn_ts + pc.h * D;
+            } else {
+                const int page = p.table[(long long)pc.s.row * p.P + pos / p.page_size], in = pos % p.page_size;
+                if (page >= 0 && page < p.num_pages) {
+                    kptr = p.kp + page * p.k_ps + in * p.k_ts + pc.h * p.k_hs;
+                    vptr = p.vp + page * p.v_ps + in * p.v_ts + pc.h * p.v_hs;
                 } else {
-                    const int page = trow[pos / p.page_size], in = pos % p.page_size;
-                    if (page >= 0 && page < p.num_pages) {
-                        kptr = p.kp + page * p.k_ps + in * p.k_ts + h * p.k_hs;
-                        vptr = p.vp + page * p.v_ps + in * p.v_ts + h * p.v_hs;
-                    } else {
-                        kvalid = false;
-                        report(p.st, DEV_BAD_ARG);
-                    }
+                    kvalid = false;
+                    report(p.st, DEV_BAD_ARG);
                 }
             }
-        };
-        auto issue = [&](int step) {
-            constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte pieces of a key, keys of one copy
-            const uint32_t kb = ring + (step % S::STAGES) * S::STAGE, vb = kb + S::TILE;
-            const int ch = lane % CPR;
+        }
+    };
+    auto issue = [&](int step) {
+        constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte pieces of a key, keys of one copy
+        const uint32_t kb = ring + (step % S::STAGES) * S::STAGE, vb = kb + S::TILE;
+        const int ch = lane % CPR;
 #pragma unroll
-            for (int i = 0; i < PA_WKEYS / RPI; ++i) {
-                const int r = i * RPI + lane / CPR;
-                const uint16_t *ks = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)kptr, r));
-                const uint16_t *vs = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)vptr, r));
-                const bool ok = __shfl_sync(0xffffffffu, (int)kvalid, r) != 0;
-                const uint32_t o = r * S::ROWB + ((ch ^ (r & 7)) << 4);
-                cp16(kb + o, ks + ch * 8, ok);
-                cp16(vb + o, vs + ch * 8, ok);
+        for (int i = 0; i < PA_WKEYS / RPI; ++i) {
+            const int r = i * RPI + lane / CPR;
+            const uint16_t *ks = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)kptr, r));
+            const uint16_t *vs = reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, (unsigned long long)vptr, r));
+            const bool ok = __shfl_sync(0xffffffffu, (int)kvalid, r) != 0;
+            const uint32_t o = r * S::ROWB + ((ch ^ (r & 7)) << 4);
+            cp16(kb + o, ks + ch * 8, ok);
+            cp16(vb + o, vs + ch * 8, ok);
+        }
+    };
+    // a piece's new tokens to their pages, and its first loads
+    auto begin = [&](const PaPiece &pc) {
+        // The new tokens' keys and values of this run go to their pages; they are read from where
+        // they came, so nothing waits for these stores.  (Row tile 0's last unit writes what no
+        // unit of it covers: a tile sees at least the first token.)
+        if (p.k_new != nullptr && pc.t == 0) {
+            const int first_new = pc.s.len - pc.s.nq;
+            const int lo = max(max(pc.off * PA_UNIT, first_new), 0);
+            const int hi = pc.off + pc.cnt == pc.units ? pc.s.len : min(pc.s.len, (pc.off + pc.cnt) * PA_UNIT);
+            constexpr int CH = D / 8;
+            for (int i = tid; i < max(hi - lo, 0) * CH; i += PA_THREADS) {
+                const int pos = lo + i / CH, ch = i % CH, tok = pc.s.q0 + pos - first_new;
+                const int page = p.table[(long long)pc.s.row * p.P + pos / p.page_size], in = pos % p.page_size;
+                if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
+                const uint4 kx = *reinterpret_cast<const uint4 *>(p.k_new + tok * p.kn_ts + pc.h * D + ch * 8);
+                const uint4 vx = *reinterpret_cast<const uint4 *>(p.v_new + tok * p.vn_ts + pc.h * D + ch * 8);
+                *reinterpret_cast<uint4 *>(p.kp + page * p.k_ps + in * p.k_ts + pc.h * p.k_hs + ch * 8) = kx;
+                *reinterpret_cast<uint4 *>(p.vp + page * p.v_ps + in * p.v_ts + pc.h * p.v_hs + ch * 8) = vx;
             }
-        };
-        locate(0);
+        }
+        locate(pc, 0);
 #pragma unroll
         for (int i = 0; i < S::STAGES - 1; ++i) {
-            if (i < cnt) issue(i);
+            if (i < pc.cnt) issue(i);
             cp_commit();
-            locate(i + 1);
+            locate(pc, i + 1);
         }
+    };
 
+    PaPiece pc;
+    pc.n = s_n;
+    pc.h = s_h;
+    pc.t = s_t;
+    pc.s = paged_seq(p, pc.n, false);
+    take(pc);
+    begin(pc);
+    for (;;) {
+        const int rows = pc.s.nq * G, first_new = pc.s.len - pc.s.nq;  // first_new may be negative: tokens without a place
         // ---- the rows' queries as mma operands, straight from memory
         uint32_t qf[D / 16][4];
         int qpos[2];  // last key that the thread's two rows see; -1: none
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = t * PA_ROWS + g8 + 8 * e;
+            const int r = pc.t * PA_ROWS + g8 + 8 * e;
             const bool ok = r < rows;
             qpos[e] = ok ? first_new + r / G : -1;
-            const uint16_t *qr = p.q + (ok ? (s.q0 + r / G) * p.q_ts + (long long)(h * G + r % G) * D : 0);
+            const uint16_t *qr = p.q + (ok ? (pc.s.q0 + r / G) * p.q_ts + (long long)(pc.h * G + r % G) * D : 0);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][e] = ok ? *reinterpret_cast<const uint32_t *>(qr + k * 16 + t4 * 2) : 0u;
                 qf[k][2 + e] = ok ? *reinterpret_cast<const uint32_t *>(qr + k * 16 + 8 + t4 * 2) : 0u;
             }
         }
-        const int low_pos = first_new + (t * PA_ROWS) / G;  // the smallest last key of the tile's rows
+        const int low_pos = first_new + (pc.t * PA_ROWS) / G;  // the smallest last key of the tile's rows
 
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-        for (int step = 0; step < cnt; ++step) {
+        for (int step = 0; step < pc.cnt; ++step) {
             cp_wait<S::STAGES - 2>();
             __syncwarp();
-            if (step + S::STAGES - 1 < cnt) issue(step + S::STAGES - 1);  // the stage read in the step before
+            if (step + S::STAGES - 1 < pc.cnt) issue(step + S::STAGES - 1);  // the stage read in the step before
             cp_commit();
-            if (step + S::STAGES < cnt) locate(step + S::STAGES);
+            if (step + S::STAGES < pc.cnt) locate(pc, step + S::STAGES);
             const uint32_t kb = ring + (step % S::STAGES) * S::STAGE, vb = kb + S::TILE;
-            const int base = (off + step) * PA_UNIT + warp * PA_WKEYS;
+            const int base = (pc.off + step) * PA_UNIT + warp * PA_WKEYS;
             float x[2][4] = {};
             {
                 const int r = (lane >> 4) * 8 + (lane & 7), hi = (lane >> 3) & 1;
@@ -311,44 +323,70 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
             }
         }
         cp_wait<0>();
+        __syncwarp();
 
-        // ---- the four warps' sums, joined in shared memory
+        // ---- the next item's loads begin before this one's sums are joined
+        const PaPiece done = pc;
+        const long long item_end = start + (WHOLE ? 1 : done.units);
+        u += WHOLE ? 1 : done.cnt;
+        const bool again = u < u_end;
+        if (again) {
+            start = item_end;
+            if (++pc.t == pa_tiles(pc.s, G)) {
+                pc.t = 0;
+                if (++pc.h == p.Hkv) {
+                    pc.h = 0;
+                    do pc.s = paged_seq(p, ++pc.n, false); while (pc.s.nq == 0);
+                }
+            }
+            take(pc);
+            begin(pc);
+        }
+
+        // ---- the four warps' sums, one after the other onto 16 rows in shared memory
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
             if (t4 == 0) s_ml[warp][g8 + 8 * e] = make_float2(m[e], l[e]);
         }
-        __syncthreads();  // every warp is done with its ring
-        float *mo = reinterpret_cast<float *>(smem);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float2 *>(mo + (warp * PA_ROWS + g8 + 8 * e) * D + i * 8 + t4 * 2) =
-                    make_float2(o[i][2 * e], o[i][2 * e + 1]);
         __syncthreads();
-        const bool begins = off == 0, ends = off + cnt == units;
+        float fw[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float M = -INFINITY;
+            for (int w = 0; w < PA_WARPS; ++w) M = fmaxf(M, s_ml[w][g8 + 8 * e].x);
+            fw[e] = ex2(m[e] - (M == -INFINITY ? 0.f : M));
+        }
+        for (int w = 0; w < PA_WARPS; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float2 *at = reinterpret_cast<float2 *>(sums + (g8 + 8 * e) * S::MSTRIDE + i * 8 + t4 * 2);
+                        float2 y = make_float2(fw[e] * o[i][2 * e], fw[e] * o[i][2 * e + 1]);
+                        if (w > 0) { const float2 z = *at; y.x += z.x; y.y += z.y; }
+                        *at = y;
+                    }
+            }
+            __syncthreads();
+        }
+        const bool begins = done.off == 0, ends = done.off + done.cnt == done.units;
         const int slot = begins ? grid + c : c;
 #pragma unroll
         for (int i = 0; i < PA_ROWS * D / 4 / PA_THREADS; ++i) {
             const int at = i * PA_THREADS + tid, r = at / (D / 4), col = (at % (D / 4)) * 4;
             float M = -INFINITY, L = 0.f;
             for (int w = 0; w < PA_WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float ref = M == -INFINITY ? 0.f : M;
-            for (int w = 0; w < PA_WARPS; ++w) {
-                const float fw = ex2(s_ml[w][r].x - ref);
-                const float4 y = *reinterpret_cast<const float4 *>(mo + (w * PA_ROWS + r) * D + col);
-                L += fw * s_ml[w][r].y;
-                a.x += fw * y.x; a.y += fw * y.y; a.z += fw * y.z; a.w += fw * y.w;
-            }
-            const int row = t * PA_ROWS + r;
+            for (int w = 0; w < PA_WARPS; ++w) L += ex2(s_ml[w][r].x - (M == -INFINITY ? 0.f : M)) * s_ml[w][r].y;
+            const float4 a = *reinterpret_cast<const float4 *>(sums + r * S::MSTRIDE + col);
+            const int row = done.t * PA_ROWS + r;
             if (begins && ends) {
-                if (row < rows) {
+                if (row < done.s.nq * G) {
                     const float inv = M == -INFINITY ? 0.f : 1.f / L;
-                    const long long tok = s.q0 + row / G;
-                    const int head = h * G + row % G;
+                    const long long tok = done.s.q0 + row / G;
+                    const int head = done.h * G + row % G;
                     uint2 y;
                     y.x = pack16x2<BF>(a.x * inv, a.y * inv);
                     y.y = pack16x2<BF>(a.z * inv, a.w * inv);
@@ -361,25 +399,13 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                 if (col == 0) p.part_ml[(long long)slot * PA_ROWS + r] = make_float2(M, L);
             }
         }
-        if (begins && !ends && tid == 0) {
+        if (!WHOLE && begins && !ends && tid == 0) {
             // runs c + 1 .. last hold the rest: the last is the one with the item's last unit
-            const long long e = start + units;
-            const int last = (int)((e * runs + W - 1) / W) - 1;
-            p.entries[c] = {n, h, t, (grid + c) * PA_ROWS, (c + 1) * PA_ROWS, last - c, PA_ROWS};
+            const int last = (int)((item_end * runs + W - 1) / W) - 1;
+            p.entries[c] = {done.n, done.h, done.t, (grid + c) * PA_ROWS, (c + 1) * PA_ROWS, last - c, PA_ROWS};
         }
+        if (!again) break;
         __syncthreads();
-
-        u += cnt;
-        if (u < u_end) {  // the next item
-            start += units;
-            if (++t == pa_tiles(s, G)) {
-                t = 0;
-                if (++h == p.Hkv) {
-                    h = 0;
-                    do s = paged_seq(p, ++n, false); while (s.nq == 0);
-                }
-            }
-        }
     }
 }
 
@@ -436,11 +462,11 @@ int paged_rows_slots(int ctas) { return 2 * ctas; }
 int paged_rows_ctas_per_sm(int d) { return d == 128 ? 2 : 3; }
 int paged_rows_tile() { return PA_ROWS; }
 
-template <int D, bool BF>
+template <int D, bool BF, bool WHOLE>
 static cudaError_t launch_rows_t(const PagedParams &p, int ctas, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, BF, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
     if (e != cudaSuccess) return e;
-    paged_rows_kernel<D, BF><<<ctas, PA_THREADS, PaShape<D>::SMEM, stream>>>(p);
+    paged_rows_kernel<D, BF, WHOLE><<<ctas, PA_THREADS, PaShape<D>::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 template <int D, bool BF>
@@ -458,9 +484,13 @@ static cudaError_t launch_join_t(const PagedParams &p, const int *count, int max
     return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF>, p, tile_rows, count, max_entries);
 }
 
-cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, int ctas, cudaStream_t stream) {
-    if (d == 128) return bf ? launch_rows_t<128, true>(p, ctas, stream) : launch_rows_t<128, false>(p, ctas, stream);
-    return bf ? launch_rows_t<64, true>(p, ctas, stream) : launch_rows_t<64, false>(p, ctas, stream);
+cudaError_t launch_paged_rows(const PagedParams &p, int d, bool bf, bool whole, int ctas, cudaStream_t stream) {
+    if (d == 128) {
+        if (whole) return bf ? launch_rows_t<128, true, true>(p, ctas, stream) : launch_rows_t<128, false, true>(p, ctas, stream);
+        return bf ? launch_rows_t<128, true, false>(p, ctas, stream) : launch_rows_t<128, false, false>(p, ctas, stream);
+    }
+    if (whole) return bf ? launch_rows_t<64, true, true>(p, ctas, stream) : launch_rows_t<64, false, true>(p, ctas, stream);
+    return bf ? launch_rows_t<64, true, false>(p, ctas, stream) : launch_rows_t<64, false, false>(p, ctas, stream);
 }
 // count: entries, on the device, or NULL for max_entries of them (some with count 0).
 cudaError_t launch_paged_join(const PagedParams &p, int d, bool bf, const int *count, int max_entries, int tile_rows, int sms,
