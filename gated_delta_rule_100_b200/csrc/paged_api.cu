@@ -90,7 +90,7 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
     }
     a.off_ml = a.off_entries + up256((size_t)a.entries * sizeof(kda::SplitEntry));
     a.off_o = a.off_ml + up256((size_t)rows * sizeof(float2));
-    a.bytes = a.off_o + (size_t)rows * d * sizeof(float) + 16;
+    a.bytes = a.whole ? 0 : a.off_o + (size_t)rows * d * sizeof(float);
     return a;
 }
 
@@ -184,7 +184,7 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
     if (dtype != KDA_BF16 && dtype != KDA_FP16) return KDA_ERR_UNSUPPORTED;
     if (!cu_q || !page_table || !length || !k_pages || !v_pages || (k_new == nullptr) != (v_new == nullptr))
         return KDA_ERR_INVALID_ARG;
-    if (total_q > 0 && (!q || !out || !workspace)) return KDA_ERR_INVALID_ARG;
+    if (total_q > 0 && (!q || !out)) return KDA_ERR_INVALID_ARG;
     const long long row = (long long)Hkv * d;
     const long long dense[6] = {page_size * row, row, d, page_size * row, row, d};
     const long long *ps = page_strides ? page_strides : dense;
@@ -199,7 +199,7 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
         return KDA_ERR_ALIGNMENT;
     if (total_q == 0) return KDA_OK;
     const AttnPlan pl = attn_plan(N, total_q, max_q, Hq, Hkv, d, page_size, P);
-    if (workspace_bytes < pl.bytes) return KDA_ERR_INVALID_ARG;
+    if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return KDA_ERR_INVALID_ARG;
     kda::PagedParams p = {};
     if (device_status(&p.st) != KDA_OK) return KDA_ERR_CUDA;
     p.q = static_cast<const uint16_t *>(q);

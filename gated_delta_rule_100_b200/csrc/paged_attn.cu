@@ -22,14 +22,18 @@
 //
 // Work is cut into equal runs of 64-key units over all (sequence, key head, row
 // tile) items, one run per CTA: lengths from 1 to the cache's end load every SM
-// alike.  A run has at most one item that began before it and one that ends
+// alike.  An item's own cost counts as PA_HEAD units: for 256 sequences of 128 to
+// 16,384 keys, 8 key heads of 128, the call took 653 us with none, 618, 596, 559
+// and 570 us with 1, 2, 4 and 8; 559 us is 6.6 TB/s, the card's copy rate.  A run has at most one item that began before it and one that ends
 // after it; these write their sums to slots, joined by the second kernel in a
 // fixed order (no atomics, so results do not depend on timing).
+#include "kda_internal.cuh"
 #include "paged_params.cuh"
 
 namespace kda {
 
 constexpr int PA_THREADS = 128, PA_WARPS = 4, PA_ROWS = 16, PA_UNIT = 64, PA_WKEYS = 16;
+constexpr int PA_HEAD = 4;  // units that an item's own cost (queries, sums, output) counts as
 
 template <int D>
 struct PaShape {
@@ -95,11 +99,11 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.G, c = blockIdx.x, grid = gridDim.x;
     launch_dependents();
-    auto plan_units = [&](const PagedSeq &s, int t) { return WHOLE ? 1 : pa_units(s, G, t); };
+    auto plan_units = [&](const PagedSeq &s, int t) { return WHOLE ? 1 : PA_HEAD + pa_units(s, G, t); };
     auto head_units = [&](const PagedSeq &s) {
         if (WHOLE) return (long long)pa_tiles(s, G);
         long long w = 0;
-        for (int t = 0; t < pa_tiles(s, G); ++t) w += pa_units(s, G, t);
+        for (int t = 0; t < pa_tiles(s, G); ++t) w += plan_units(s, t);
         return w;
     };
 
@@ -148,11 +152,14 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
     float *sums = reinterpret_cast<float *>(smem + PA_WARPS * S::RING);
     const int g8 = lane >> 2, t4 = lane & 3;
 
-    // the run's part of the item at unit u, which begins at unit `start`
+    // the run's part of the item that unit u lies in and that begins at unit `start`: its first
+    // PA_HEAD units stand for no keys, so a part may be empty
     auto take = [&](PaPiece &pc) {
         pc.units = pa_units(pc.s, G, pc.t);
-        pc.off = WHOLE ? 0 : (int)(u - start);
-        pc.cnt = WHOLE ? pc.units : (int)min((long long)(pc.units - pc.off), u_end - u);
+        const int to = (int)min((long long)(PA_HEAD + pc.units), u_end - start);
+        pc.off = WHOLE ? 0 : max(0, (int)(u - start) - PA_HEAD);
+        pc.cnt = WHOLE ? pc.units : max(0, to - PA_HEAD) - pc.off;
+        u = WHOLE ? u + 1 : start + to;
     };
     // ---- the warp's loads: 16 keys of each unit
     const uint16_t *kptr = p.kp, *vptr = p.vp;
@@ -229,6 +236,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
     pc.t = s_t;
     pc.s = paged_seq(p, pc.n, false);
     take(pc);
+    if (pc.cnt == 0) return;
     begin(pc);
     for (;;) {
         const int rows = pc.s.nq * G, first_new = pc.s.len - pc.s.nq;  // first_new may be negative: tokens without a place
@@ -327,9 +335,8 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
 
         // ---- the next item's loads begin before this one's sums are joined
         const PaPiece done = pc;
-        const long long item_end = start + (WHOLE ? 1 : done.units);
-        u += WHOLE ? 1 : done.cnt;
-        const bool again = u < u_end;
+        const long long item_end = start + (WHOLE ? 1 : PA_HEAD + done.units);
+        bool again = u < u_end;
         if (again) {
             start = item_end;
             if (++pc.t == pa_tiles(pc.s, G)) {
@@ -340,7 +347,8 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                 }
             }
             take(pc);
-            begin(pc);
+            again = pc.cnt > 0;
+            if (again) begin(pc);
         }
 
         // ---- the four warps' sums, one after the other onto 16 rows in shared memory
@@ -464,7 +472,7 @@ int paged_rows_tile() { return PA_ROWS; }
 
 template <int D, bool BF, bool WHOLE>
 static cudaError_t launch_rows_t(const PagedParams &p, int ctas, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<D, BF, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
+    const cudaError_t e = allow_smem(paged_rows_kernel<D, BF, WHOLE>, PaShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     paged_rows_kernel<D, BF, WHOLE><<<ctas, PA_THREADS, PaShape<D>::SMEM, stream>>>(p);
     return cudaGetLastError();

@@ -873,7 +873,7 @@ static bool page_map(CUtensorMap *map, PFN_cuTensorMapEncodeTiled_v12000 enc, co
 
 template <int D, bool BF>
 static cudaError_t launch_chunk_t(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &c, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, CkShape<D>::SMEM);
+    cudaError_t e = allow_smem(paged_chunk_kernel<D, BF>, CkShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     // one block plans; with new tokens to place, two an SM place them meanwhile
     const long long vecs = (long long)c.p.total_q * c.p.Hkv * (D / 8), blocks = (vecs + 511) / 512;

@@ -15,6 +15,7 @@
 #include <cooperative_groups.h>
 #include <stddef.h>
 
+#include "kda_internal.cuh"
 #include "pages_params.cuh"
 
 namespace kda {
@@ -446,7 +447,8 @@ cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t str
     auto *k = fork ? pages_grant_kernel<true> : pages_grant_kernel<false>;
     const size_t smem = grant_bytes(p.n);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grant_bytes(PG_MAX_LIST));
+        const cudaError_t e = fork ? allow_smem(pages_grant_kernel<true>, (int)grant_bytes(PG_MAX_LIST))
+                                   : allow_smem(pages_grant_kernel<false>, (int)grant_bytes(PG_MAX_LIST));
         if (e != cudaSuccess) return e;
     }
     return launch_behind(k, dim3(PG_CLUSTER), PG_THREADS, smem, stream, p);

@@ -535,51 +535,58 @@ def _there(t, stream):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _arr(t, name, dtype, shape, device):
-    """The address of a contiguous tensor that is what the call needs."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+def _arr(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor that is what the call needs, on device index dev."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _check(t, name, dtype, shape)
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
     return t.data_ptr()
 
 
-def _like(t, name, dtype, shape, device):
+def _like(t, name, dtype, shape, dev):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on device {dev}, got {t.device}")
 
 
-def _token_stride(t, name, dtype, shape, device):
+def _token_stride(t, name, dtype, shape, dev):
     """Elements between the tokens of a [tokens, heads, d] tensor, which may lie apart (a slice
     of a fused projection)."""
-    _like(t, name, dtype, shape, device)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _like(t, name, dtype, shape, dev)
+    st, sh, sd = t.stride()
     n, h, d = shape
-    st = t.stride()
-    if n and (st[2] != 1 or (h > 1 and st[1] != d)):
+    if n and (sd != 1 or (h > 1 and sh != d)):
         raise ValueError(f"{name}: heads and channels must be contiguous")
-    return st[0] if n > 1 else h * d
+    return st if n > 1 else h * d
 
 
-def _page_strides(t, name, dtype, shape, device):
+def _page_strides(t, name, dtype, shape, dev):
     """Elements between the pages, tokens and heads of a pool of pages."""
-    _like(t, name, dtype, shape, device)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _like(t, name, dtype, shape, dev)
     sp, st, sh, sd = t.stride()
     n, ps, h, d = shape
     # a stride along one entry says nothing; give it the dense value
-    sh, st, sp = (sh if h > 1 else d), (st if ps > 1 else h * d), (sp if n > 1 else ps * h * d)
+    if h == 1:
+        sh = d
+    if ps == 1:
+        st = h * d
+    if n == 1:
+        sp = ps * h * d
     if sd != 1 or sh < d or st < d or sp < d:
         raise ValueError(f"{name}: channels must be contiguous, and tokens, heads and pages not overlap")
     return sp, st, sh
 
 
 _attn_bytes = {}
+_Strides = ctypes.c_longlong * 6
 
 
 def paged_attn_workspace_bytes(N, total_q, max_q, Hq, Hkv, d, page_size, P) -> int:
@@ -597,8 +604,8 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
     int32 [N] or None (rows 0..N-1); max_q the most new tokens that a sequence has.  k_new,
     v_new [total_q,Hkv,d] are written to their pages first; without them the cache holds them.
     Returns out [total_q,Hq,d]; lse fp32 [total_q,Hq] is written when given."""
-    dt = q.dtype
-    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or cu_q.dim() != 1 or cu_q.numel() < 2:
+    dt, shape, pages, table, N = q.dtype, q.shape, k_pages.shape, page_table.shape, cu_q.numel() - 1
+    if len(shape) != 3 or len(pages) != 4 or len(table) != 2 or cu_q.dim() != 1 or N < 1:
         raise ValueError("q must be [total_q,Hq,d], k_pages [num_pages,page_size,Hkv,d], page_table [R,P], cu_q [N+1]")
     if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError(f"q must be bfloat16 or float16, got {dt}")
@@ -606,18 +613,16 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
         with _there(q, stream):
             return paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, max_q=max_q, k_new=k_new, v_new=v_new,
                               rows=rows, out=out, lse=lse)
-    dev, shape = q.device, q.shape
+    dev, i32 = q.get_device(), torch.int32
     total, Hq, d = shape
-    pages = k_pages.shape
-    num_pages, ps, Hkv, _ = pages
-    R, P = page_table.shape
-    N = cu_q.numel() - 1
-    i32 = torch.int32
+    num_pages, ps, Hkv, dp = pages
+    R, P = table
+    if dp != d:
+        raise ValueError(f"k_pages must have {d} channels, got {dp}")
     qs = _token_stride(q, "q", dt, shape, dev)
-    strides = _page_strides(k_pages, "k_pages", dt, (num_pages, ps, Hkv, d), dev) \
-        + _page_strides(v_pages, "v_pages", dt, (num_pages, ps, Hkv, d), dev)
+    strides = _page_strides(k_pages, "k_pages", dt, pages, dev) + _page_strides(v_pages, "v_pages", dt, pages, dev)
     cu = _arr(cu_q, "cu_q", i32, (N + 1,), dev)
-    tab = _arr(page_table, "page_table", i32, (R, P), dev)
+    tab = _arr(page_table, "page_table", i32, table, dev)
     ln = _arr(length, "length", i32, (R,), dev)
     rw = None if rows is None else _arr(rows, "rows", i32, (N,), dev)
     if (k_new is None) != (v_new is None):
@@ -630,8 +635,10 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
         kp, vp = k_new.data_ptr(), v_new.data_ptr()
     ls = None if lse is None else _arr(lse, "lse", torch.float32, (total, Hq), dev)
     if out is None:
-        out = torch.empty(shape, device=dev, dtype=dt)
-    op = _arr(out, "out", dt, shape, dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op = out.data_ptr()
+    else:
+        op = _arr(out, "out", dt, shape, dev)
     lib = load()
     key = (dev, N, total, max_q, Hq, Hkv, d, ps, P)
     nbytes = _attn_bytes.get(key)
@@ -639,10 +646,10 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
         if len(_attn_bytes) > 4096:
             _attn_bytes.clear()
         nbytes = _attn_bytes[key] = paged_attn_workspace_bytes(*key[1:])
-    ws = torch.empty(nbytes or 1, device=dev, dtype=torch.uint8)
+    ws = torch.empty(nbytes, device=q.device, dtype=torch.uint8) if nbytes else None
     rc = lib.kda_paged_attn(q.data_ptr(), kp, vp, k_pages.data_ptr(), v_pages.data_ptr(), cu, tab, ln, rw, scale, op, ls,
-                            N, total, max_q, Hq, Hkv, d, ps, num_pages, P, R, qs, ks, vs, (ctypes.c_longlong * 6)(*strides),
-                            0 if dt is torch.bfloat16 else 1, ws.data_ptr(), nbytes, _raw_stream(q))
+                            N, total, max_q, Hq, Hkv, d, ps, num_pages, P, R, qs, ks, vs, _Strides(*strides),
+                            0 if dt is torch.bfloat16 else 1, ws.data_ptr() if nbytes else None, nbytes, _raw_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_paged_attn")
     return out
@@ -662,8 +669,8 @@ def _cache(table, length, ref, info, dev):
 def _pool(t, num_pages, dev):
     """(pointer, outer, outer stride, page stride, page bytes) of a pool [outer, num_pages, ...]
     whose pages are contiguous; strides in bytes."""
-    if t.device != dev:
-        raise ValueError(f"a pool must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"a pool must be on device {dev}, got {t.device}")
     shape, st = t.shape, t.stride()
     if len(shape) < 3 or shape[1] != num_pages:
         raise ValueError(f"a pool must be [outer, {num_pages}, ...], got {tuple(shape)}")
@@ -685,36 +692,36 @@ def pages_reserve(table, length, ref, rows, new_length, page_size, *, info=None,
     if not _here(table, stream):
         with _there(table, stream):
             return pages_reserve(table, length, ref, rows, new_length, page_size, info=info)
-    dev, n = table.device, rows.numel()
+    dev, n = table.get_device(), rows.numel()
     t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
     rc = load().kda_pages_reserve(t, ln, rf, _arr(rows, "rows", torch.int32, (n,), dev),
                                   _arr(new_length, "new_length", torch.int32, (n,), dev), n, inf, R, P, pages, page_size,
-                                  _raw_stream(table))
+                                  _raw_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_reserve")
 
 
 def pages_fork(table, length, ref, src, dst, page_size, *, pools=(), info=None, stream=None):
     """Empty rows dst (int32 [n]) share the sequences of rows src: full pages by count, a
-    partial last page copied in every pool [outer, num_pages, ...].  Returns (copy_src,
-    copy_dst), int32 [n], the pages copied (-1, -1: none).  info as ``pages_reserve``."""
+    partial last page copied in every pool [outer, num_pages, ...].  Returns int32 [2,n],
+    the pages copied, from and to (-1, -1: none).  info as ``pages_reserve``."""
     if not _here(table, stream):
         with _there(table, stream):
             return pages_fork(table, length, ref, src, dst, page_size, pools=pools, info=info)
-    dev, n = table.device, src.numel()
+    dev, n = table.get_device(), src.numel()
     t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
     args = [_pool(x, pages, dev) for x in pools]
     a, b = _arr(src, "src", torch.int32, (n,), dev), _arr(dst, "dst", torch.int32, (n,), dev)
-    cs, cd = torch.empty((2, n), device=dev, dtype=torch.int32).unbind(0)
-    lib, st = load(), _raw_stream(table)
-    rc = lib.kda_pages_fork(t, ln, rf, a, b, n, cs.data_ptr(), cd.data_ptr(), inf, R, P, pages, page_size, st)
+    pairs = torch.empty((2, n), device=table.device, dtype=torch.int32)
+    lib, st, cs = load(), _raw_stream(dev), pairs.data_ptr()
+    rc = lib.kda_pages_fork(t, ln, rf, a, b, n, cs, cs + 4 * n, inf, R, P, pages, page_size, st)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_fork")
     for x in args:
-        rc = lib.kda_pages_copy(*x, pages, cs.data_ptr(), cd.data_ptr(), n, st)
+        rc = lib.kda_pages_copy(*x, pages, cs, cs + 4 * n, n, st)
         if rc != KDA_OK:
             raise KdaError(rc, "kda_pages_copy")
-    return cs, cd
+    return pairs
 
 
 def pages_free(table, length, ref, rows, page_size, *, stream=None):
@@ -722,10 +729,10 @@ def pages_free(table, length, ref, rows, page_size, *, stream=None):
     if not _here(table, stream):
         with _there(table, stream):
             return pages_free(table, length, ref, rows, page_size)
-    dev, n = table.device, rows.numel()
+    dev, n = table.get_device(), rows.numel()
     t, ln, rf, _, R, P, pages = _cache(table, length, ref, None, dev)
     rc = load().kda_pages_free(t, ln, rf, _arr(rows, "rows", torch.int32, (n,), dev), n, R, P, pages, page_size,
-                               _raw_stream(table))
+                               _raw_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_free")
 
@@ -737,15 +744,15 @@ def pages_compact(table, length, ref, page_size, *, table_out=None, ref_out=None
     if not _here(table, stream):
         with _there(table, stream):
             return pages_compact(table, length, ref, page_size, table_out=table_out, ref_out=ref_out, pools=pools, info=info)
-    dev = table.device
+    dev = table.get_device()
     t, ln, rf, inf, R, P, pages = _cache(table, length, ref, info, dev)
     table_out = table if table_out is None else table_out
     ref_out = ref if ref_out is None else ref_out
     to, ro = _arr(table_out, "table_out", torch.int32, (R, P), dev), _arr(ref_out, "ref_out", torch.int32, (pages,), dev)
     args = [_pool(x, pages, dev) for x in pools]
-    lib, st = load(), _raw_stream(table)
+    lib, st = load(), _raw_stream(dev)
     nbytes = lib.kda_pages_compact_workspace_bytes(pages)
-    ws = torch.empty(max(nbytes, 1), device=dev, dtype=torch.uint8)
+    ws = torch.empty(nbytes, device=table.device, dtype=torch.uint8)
     rc = lib.kda_pages_compact(t, ln, rf, to, ro, inf, R, P, pages, page_size, ws.data_ptr(), nbytes, st)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_compact")
@@ -764,8 +771,8 @@ def pages_copy(pool, src, dst, *, stream=None):
             return pages_copy(pool, src, dst)
     if pool.dim() < 3:
         raise ValueError("a pool must be [outer, num_pages, ...]")
-    dev, pages, n = pool.device, pool.shape[1], src.numel()
+    dev, pages, n = pool.get_device(), pool.shape[1], src.numel()
     rc = load().kda_pages_copy(*_pool(pool, pages, dev), pages, _arr(src, "src", torch.int32, (n,), dev),
-                               _arr(dst, "dst", torch.int32, (n,), dev), n, _raw_stream(pool))
+                               _arr(dst, "dst", torch.int32, (n,), dev), n, _raw_stream(dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_pages_copy")

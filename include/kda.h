@@ -420,8 +420,8 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  *                k_pages, then of v_pages; NULL for the dense layout above
  *   dtype      : KDA_BF16 or KDA_FP16, of q, k, v and out
  *   workspace  : kda_paged_attn_workspace_bytes() bytes, 16-byte aligned, of
- *                the caller; a call's alone until it is done, contents of no
- *                consequence before and after
+ *                the caller (NULL when that is 0); a call's alone until it is
+ *                done, contents of no consequence before and after
  *
  * Token i of sequence n, of n_q new ones, is at position p = length - n_q + i.
  * It attends keys 0 .. p: o = sum_j softmax_j(scale q.k_j) v_j, query head h
@@ -449,7 +449,7 @@ KDA_API int kda_paged_attn(const void *q, const void *k_new, const void *v_new,
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* Workspace of kda_paged_attn for these sizes on the current device (0 when
- * they are unsupported or total_q == 0). */
+ * none is needed, the sizes are unsupported or total_q == 0). */
 KDA_API size_t kda_paged_attn_workspace_bytes(int N, int total_q, int max_q, int Hq, int Hkv, int d,
                   int page_size, int P);
 

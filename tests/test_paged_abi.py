@@ -20,7 +20,7 @@ def lib():
 
 
 def attn(lib, q=A, k_new=A, v_new=A, kp=A, vp=A, cu=A, table=A, length=A, rows=None, scale=0.125, out=A, lse=None, N=2,
-         total=5, max_q=4, Hq=8, Hkv=2, d=64, ps=16, pages=9, P=4, R=2, qs=None, ks=None, vs=None, strides=None,
+         total=5, max_q=4, Hq=8, Hkv=2, d=64, ps=16, pages=9, P=40, R=2, qs=None, ks=None, vs=None, strides=None,
          dtype=0, ws=A, nbytes=1 << 40):
     st = None if strides is None else (ctypes.c_longlong * 6)(*strides)
     return lib.kda_paged_attn(q, k_new, v_new, kp, vp, cu, table, length, rows, scale, out, lse, N, total, max_q, Hq, Hkv,
@@ -48,7 +48,8 @@ def test_no_tokens_need_nothing(lib):
     assert attn(lib, total=0, max_q=0, q=None, out=None, k_new=None, v_new=None, ws=None, nbytes=0) == kda.KDA_OK
     assert kda.paged_attn_workspace_bytes(2, 0, 0, 8, 2, 64, 16, 4) == 0
     assert kda.paged_attn_workspace_bytes(2, 5, 4, 8, 2, 96, 16, 4) == 0
-    assert kda.paged_attn_workspace_bytes(2, 5, 4, 8, 2, 64, 16, 4) > 0
+    assert kda.paged_attn_workspace_bytes(2, 5, 4, 8, 2, 64, 16, 40) > 0
+    assert kda.paged_attn_workspace_bytes(2, 50, 48, 8, 2, 64, 16, 4) > 0
 
 
 def reserve(lib, table=A, length=A, ref=A, rows=A, new=A, n=2, info=None, R=4, P=4, pages=9, ps=16):

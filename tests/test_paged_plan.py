@@ -5,9 +5,11 @@ import random
 import pytest
 
 
-def runs_model(units, grid):
-    """units: per item.  Returns per item the set of unit ranges written in full, and the
-    slots joined, as paged_attn.cu lays them out."""
+def runs_model(real, grid, head):
+    """real: units of keys per item; head: units that stand for an item's own cost.  Returns
+    per item the unit ranges written in full, and the slots joined, as paged_attn.cu lays
+    them out."""
+    units = [head + x for x in real]
     W = sum(units)
     starts = [sum(units[:i]) for i in range(len(units))]
     runs = min(W, grid)
@@ -16,12 +18,17 @@ def runs_model(units, grid):
         u, end = c * W // runs, (c + 1) * W // runs
         assert u < end
         while u < end:
-            i = max(k for k in range(len(units)) if starts[k] <= u and units[k] > 0)
-            off = u - starts[i]
-            cnt = min(units[i] - off, end - u)
-            begins, ends = off == 0, off + cnt == units[i]
+            i = max(k for k in range(len(units)) if starts[k] <= u)
+            to = min(units[i], end - starts[i])
+            off = max(0, u - starts[i] - head)
+            cnt = max(0, to - head) - off
+            u = starts[i] + to
+            if cnt == 0:
+                assert u == end  # a part without keys is a run's last, or all of it
+                continue
+            begins, ends = off == 0, off + cnt == real[i]
             if begins and ends:
-                whole[i] = (0, units[i])
+                whole[i] = (0, real[i])
             else:
                 slot = grid + c if begins else c
                 assert slot not in pieces and slot < 2 * grid
@@ -30,16 +37,16 @@ def runs_model(units, grid):
                     last = ((starts[i] + units[i]) * runs + W - 1) // W - 1
                     assert c not in entries
                     entries[c] = (i, grid + c, c + 1, last - c)
-            u += cnt
     return whole, pieces, entries
 
 
+@pytest.mark.parametrize("head", [0, 1, 2, 5])
 @pytest.mark.parametrize("seed", range(40))
-def test_runs_cover_every_item_once(seed):
+def test_runs_cover_every_item_once(seed, head):
     r = random.Random(seed)
     units = [r.choice([1, 1, 2, 3, r.randint(1, 60)]) for _ in range(r.randint(1, 40))]
     grid = r.choice([1, 2, 3, 7, 24, 100])
-    whole, pieces, entries = runs_model(units, grid)
+    whole, pieces, entries = runs_model(units, grid, head)
     joined = {}
     for i, head, nxt, count in entries.values():
         assert i not in joined and i not in whole and count >= 1
