@@ -72,7 +72,7 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
         a.tile = kda::paged_chunk_tile();
         a.lim = kda::paged_chunk_limits(N, total_q, G, Hkv, P * page_size, a.sms);
         a.entries = a.lim.entries;
-        a.off_entries = 256 + up256((size_t)N * sizeof(int2)) + up256((size_t)a.lim.pieces * kda::paged_chunk_piece_bytes());
+        a.off_entries = 256 + up256(3 * (size_t)N * sizeof(int)) + up256((size_t)a.lim.pieces * kda::paged_chunk_piece_bytes());
         rows = a.lim.rows;
     } else {
         a.tile = kda::paged_rows_tile();

@@ -54,7 +54,7 @@ struct ChunkParams {
     PagedParams p;
     ChunkPlanHead *head;
     ChunkPiece *pieces;
-    int2 *base;            // [N] the plan's scratch
+    int *base;             // [3][N] the plan's scratch
     int max_pieces, max_entries, max_rows, sms;
 };
 
@@ -93,10 +93,10 @@ __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 1
 __device__ void ck_plan(const ChunkParams &c, int d) {
     __shared__ unsigned long long s_w;
     __shared__ unsigned s_wa, s_a, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // pieces and eighths of rows of one key head
-    __shared__ int s_max, s_items, s_step, s_phi, s_entries, s_part, s_sum[2][33];
+    __shared__ int s_max, s_ma, s_items, s_step, s_phi, s_entries, s_part, s_sum[33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
-    if (tid == 0) { s_w = 0; s_wa = s_a = 0; s_max = 1; s_items = s_entries = s_part = 0; }
+    if (tid == 0) { s_w = 0; s_wa = s_a = 0; s_max = 1; s_ma = s_items = s_entries = s_part = 0; }
     if (tid < 2 * CK_CAND) s_pieces[tid] = s_rows8[tid] = 0;
     __syncthreads();
     // a warp a sequence, a lane a row tile
@@ -134,13 +134,14 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
         const int q = lane / CK_CAND, split = max(1, warps / p.N);
         const float inv = 1.f / ((s_max + ck_div[lane % CK_CAND] - 1) / ck_div[lane % CK_CAND]);
         unsigned pieces = 0, rows8 = 0, wa = 0, na = 0;
+        int ma = 0;
         for (int v = warp; v < p.N * split; v += warps) {
             const PagedSeq s = paged_seq(p, v % p.N, false);
             const int tiles = ck_tiles(s, G), a = whole(tiles, 1);
             for (int t = v / p.N; t < tiles; t += split) {
                 const int k = ck_keys(s, G, t), ns = (int)ceilf(k * inv - 1e-3f);  // near enough for the choice
                 const bool in_a = tiles - 1 - t < a;
-                if (in_a) { wa += k; ++na; }
+                if (in_a) { wa += k; ++na; ma = max(ma, k); }
                 if (!(q && in_a)) {
                     pieces += ns;
                     if (ns > 1) rows8 += ns * ((ck_rows(s, G, t) + 7) / 8);
@@ -152,6 +153,7 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
         if (lane == 0) {
             atomicAdd(&s_wa, wa);
             atomicAdd(&s_a, na);
+            atomicMax(&s_ma, ma);
         }
     }
     __syncthreads();
@@ -161,7 +163,8 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
         const float pa = q ? (float)s_a * p.Hkv : 0.f, ta = q && s_a ? (float)s_wa / s_a + 3.f : 0.f;
         const float pb = (float)s_pieces[lane] * p.Hkv, tb = pb > 0.f ? (float)(s_w - (q ? s_wa : 0)) * p.Hkv / pb + 3.f : 3.f;
         const float ka = ceilf(pa / S), early = (ka * S - pa) * floorf(ta / tb);
-        float cost = ka * ta + (pb > early ? fmaxf(ceilf((pb - early) / S) * tb, fminf(step + 3.f, tb * 2.f)) : 0.f);
+        float cost = ka * ta + (pb > early ? ceilf((pb - early) / S) * tb : 0.f);
+        cost = fmaxf(cost, max(pa > 0.f ? s_ma : 0, pb > 0.f ? step : 0) + 3.f);  // no less than the longest
         if (R > 0.f) cost += 3.f + R * d * 8.f * 1.2e-7f;
         if (lane > 0 && (pa + pb > c.max_pieces || R > c.max_rows)) cost = 3.0e38f;
         float best = cost;
@@ -172,66 +175,71 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     }
     __syncthreads();
     const int step = s_step, phi = s_phi;
-    // pieces per key head of a sequence, whole ones and others; then where each sequence's begin:
-    // every whole item first
+    // The order of the pieces, for CTAs that claim them one by one: whole items, then pieces of the
+    // full length and rests of half of it, then the other rests, so that what is claimed last is short.  Pieces of each kind per key
+    // head of a sequence; then where each sequence's begin.
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, false);
         const int tiles = ck_tiles(s, G), a = whole(tiles, phi);
-        int k = 0;
-        for (int t = lane; t < tiles - a; t += 32) k += (ck_keys(s, G, t) + step - 1) / step;
-        k = __reduce_add_sync(0xffffffffu, k);
-        if (lane == 0) c.base[n] = make_int2(a * p.Hkv, k * p.Hkv);
+        int full = 0, rest = 0;
+        for (int t = lane; t < tiles - a; t += 32) {
+            const int k = ck_keys(s, G, t);
+            const int big = 2 * (k % step) >= step;
+            full += k / step + big;
+            rest += !big && k % step != 0;
+        }
+        full = __reduce_add_sync(0xffffffffu, full);
+        rest = __reduce_add_sync(0xffffffffu, rest);
+        if (lane == 0) {
+            c.base[n] = a * p.Hkv;
+            c.base[n + p.N] = full * p.Hkv;
+            c.base[n + 2 * p.N] = rest * p.Hkv;
+        }
     }
     __syncthreads();
-    const int per = (p.N + blockDim.x - 1) / blockDim.x;
-    int mine[2] = {0, 0}, at[2], total[2] = {0, 0};
-    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) { mine[0] += c.base[n].x; mine[1] += c.base[n].y; }
+    const int cells = 3 * p.N, per = (cells + blockDim.x - 1) / blockDim.x;
+    int mine = 0;
+    for (int n = tid * per; n < min(cells, (tid + 1) * per); ++n) mine += c.base[n];
+    int incl = mine, total = 0;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        int incl = mine[q];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        if (lane == 31) s_sum[q][warp] = incl;
-        at[q] = incl - mine[q];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
     }
+    if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        for (int k = 0; k < warps; ++k) {
-            if (k < warp) at[q] += s_sum[q][k];
-            total[q] += s_sum[q][k];
-        }
-    at[1] += total[0];
-    for (int n = tid * per; n < min(p.N, (tid + 1) * per); ++n) {
-        const int2 k = c.base[n];
-        c.base[n] = make_int2(at[0], at[1]);
-        at[0] += k.x;
-        at[1] += k.y;
+    int at = incl - mine;
+    for (int k = 0; k < warps; ++k) {
+        if (k < warp) at += s_sum[k];
+        total += s_sum[k];
+    }
+    for (int n = tid * per; n < min(cells, (tid + 1) * per); ++n) {
+        const int k = c.base[n];
+        c.base[n] = at;
+        at += k;
     }
     __syncthreads();
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, false);
         const int tiles = ck_tiles(s, G), a = whole(tiles, phi);
-        const int2 first = c.base[n];
-        const int per_head = ((n + 1 < p.N ? c.base[n + 1].y : total[0] + total[1]) - first.y) / p.Hkv;
-        int before = 0;
+        const int f0 = c.base[n + p.N], r0 = c.base[n + 2 * p.N];
+        const int full_head = (c.base[n + p.N + 1] - f0) / p.Hkv;
+        const int rest_head = ((n + 1 < p.N ? c.base[n + 2 * p.N + 1] : total) - r0) / p.Hkv;
+        int full_before = 0, rest_before = 0;
         for (int t0 = 0; t0 < tiles; t0 += 32) {
             const int rank = t0 + lane, t = tiles - 1 - rank;  // the longest first
             const bool w1 = rank < a;
-            const int k = t >= 0 ? ck_keys(s, G, t) : 0, st = w1 ? k : step, ns = t >= 0 ? (k + st - 1) / st : 0;
-            int inc = w1 ? 0 : ns;
+            const int k = t >= 0 ? ck_keys(s, G, t) : 0, big = 2 * (k % step) >= step,
+                      full = w1 ? 0 : k / step + big, rest = !w1 && !big && k % step != 0;
+            int fi = full, ri = rest;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += up;
+                const int uf = __shfl_up_sync(0xffffffffu, fi, o), ur = __shfl_up_sync(0xffffffffu, ri, o);
+                if (lane >= o) { fi += uf; ri += ur; }
             }
             if (t >= 0) {
-                const int r = ck_rows(s, G, t);
+                const int r = ck_rows(s, G, t), ns = w1 ? 1 : full + rest;
                 for (int h = 0; h < p.Hkv; ++h) {
-                    const long long i = w1 ? first.x + (long long)h * a + rank : first.y + (long long)h * per_head + before + inc - ns;
                     int part = -1;
                     if (ns > 1) {
                         part = atomicAdd(&s_part, ns * r);
@@ -241,20 +249,24 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
                         else report(p.st, DEV_BAD_ARG);  // only where sequences overlap
                     }
                     for (int j = 0; j < ns; ++j) {
-                        if (i + j >= c.max_pieces) { report(p.st, DEV_BAD_ARG); break; }
-                        const int row = part < 0 ? -1 : part + j * r;
+                        const long long i = w1 ? (long long)c.base[n] + (long long)h * a + rank
+                                          : j < full ? f0 + (long long)h * full_head + full_before + fi - full + j
+                                                     : r0 + (long long)h * rest_head + rest_before + ri - 1;
+                        if (i >= c.max_pieces) { report(p.st, DEV_BAD_ARG); continue; }
+                        const int kv0 = j * step, row = part < 0 ? -1 : part + j * r;
                         // a piece without room for its sums is left empty
                         const bool room = part < 0 || part + ns * r <= c.max_rows;
-                        c.pieces[i + j] = {n, h, t, j * st, room ? min(k, (j + 1) * st) : j * st, row, s, {0, 0}};
+                        c.pieces[i] = {n, h, t, kv0, !room ? kv0 : w1 ? k : min(k, kv0 + step), row, s, {0, 0}};
                     }
                 }
             }
-            before += __shfl_sync(0xffffffffu, inc, 31);
+            full_before += __shfl_sync(0xffffffffu, fi, 31);
+            rest_before += __shfl_sync(0xffffffffu, ri, 31);
         }
     }
     __syncthreads();
     if (tid == 0) {
-        c.head->pieces = min(total[0] + total[1], c.max_pieces);
+        c.head->pieces = min(total, c.max_pieces);
         c.head->ticket = 0;
         c.head->entries = min(s_entries, c.max_entries);
     }
@@ -687,7 +699,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const bool real = w * CK_M + r < rows;
                 key0 = pc.kv0 * CK_KT;
                 last = sq.len - sq.nq + tok;
-                if (!real) { last = 0x7fffffff; m = 0.f; }  // no row: nothing to mask, a reference that never moves
+                if (!real) { last = 0x7ffffff0; m = 0.f; }  // no row: nothing to mask, a reference that never moves
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     p.q + (real ? (sq.q0 + tok) * p.q_ts + (long long)(pc.h * G + row % G) * D : 0));
                 uint4 x[D / 8];  // its query, to the swizzled tile
@@ -893,7 +905,7 @@ static cudaError_t launch_chunk_t(const CUtensorMap &tk, const CUtensorMap &tv, 
     return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<D, BF>, tk, tv, c);
 }
 
-// ws: the plan's part of the workspace: head (256 bytes), base [N] (8 bytes each), pieces.
+// ws: the plan's part of the workspace: head (256 bytes), base [3][N], pieces.
 cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void *ws, int d, bool bf, int sms, cudaStream_t stream) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     if (host_encoder(&enc) != 0) return cudaErrorUnknown;
@@ -904,8 +916,8 @@ cudaError_t launch_paged_chunk(const PagedParams &p, const ChunkLimits &m, void 
     ChunkParams c;
     c.p = p;
     c.head = static_cast<ChunkPlanHead *>(ws);
-    c.base = reinterpret_cast<int2 *>(static_cast<uint8_t *>(ws) + 256);
-    c.pieces = reinterpret_cast<ChunkPiece *>(reinterpret_cast<uint8_t *>(c.base) + ((size_t)p.N * 8 + 255) / 256 * 256);
+    c.base = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + 256);
+    c.pieces = reinterpret_cast<ChunkPiece *>(reinterpret_cast<uint8_t *>(c.base) + ((size_t)p.N * 12 + 255) / 256 * 256);
     c.max_pieces = m.pieces;
     c.max_entries = m.entries;
     c.max_rows = m.rows;

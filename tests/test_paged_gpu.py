@@ -242,6 +242,23 @@ def test_bad_numbers_are_reported(what, nq, ln):
         assert (t[0] == v).all() and (t[-1] == v).all()
 
 
+@pytest.mark.parametrize("nq,ln", [([300, 2], [900, 70]), ([1, 1], [9000, 70])], ids=["chunk", "few"])
+def test_waits_that_give_up_are_reported(nq, ln):
+    """With no patience at all the chunk kernel's waits run out; the call ends, says so, and the next one works."""
+    c = make(nq, ln, 8, 2, 128, 64, seed=2)
+    kp, vp = appended(c)
+    try:
+        kda.set_wait_limit(1)
+        call(c)
+        status = kda.stream_status()
+    finally:
+        kda.set_wait_limit(0)
+    assert status == (kda.KDA_ERR_TIMEOUT if max(nq) > 1 else kda.KDA_OK)
+    out, lse = call(c)
+    assert kda.stream_status() == kda.KDA_OK
+    check(c, out, lse, kp, vp)
+
+
 def test_refusals():
     c = make([1], [9], 4, 2, 64, 16)
     ok = lambda **kw: kda.paged_attn(*[kw.get(k, c[k]) for k in ("q", "kp", "vp", "cu", "table", "length")], 0.125,  # noqa: E731
