@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
 
 // Joins the pieces of split items, one warp per row: entries in turn over
 // blockIdx.x, rows over blockIdx.y.  The pieces have just been written and lie
-// in L2, so a lane keeps four loads in flight and that is enough.
+// in L2: what a row costs is the round trip to it.
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, int tile_rows, const int *count, int max_entries) {
     wait_for_primary();
@@ -432,24 +432,35 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
         const int rows = min(tile_rows, s.nq * p.G - e.t * tile_rows);
         for (int r = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
             auto at = [&](int k) { return (long long)(k == 0 ? e.head : e.next + (k - 1) * e.stride) + r; };
-            float M = -INFINITY;
-            for (int k = lane; k <= e.count; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float ref = M == -INFINITY ? 0.f : M;
+            // pieces four at a time with a running maximum, so that a row's loads are one round trip
             constexpr int V = D / 32;
-            float a[V] = {}, L = 0.f;
-#pragma unroll 4
-            for (int k = 0; k <= e.count; ++k) {
-                const float2 ml = p.part_ml[at(k)];
-                const float f = ex2(ml.x - ref);
-                L += f * ml.y;
-                const float *src = p.part_o + at(k) * D + lane * V;
+            float M = -INFINITY, L = 0.f, a[V] = {};
+            for (int k0 = 0; k0 <= e.count; k0 += 4) {
+                float2 ml[4], y[4][V / 2];
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float2 y = *reinterpret_cast<const float2 *>(src + j);
-                    a[j] += f * y.x;
-                    a[j + 1] += f * y.y;
+                for (int k = 0; k < 4; ++k) {
+                    const bool in = k0 + k <= e.count;
+                    const long long x = at(in ? k0 + k : k0);
+                    ml[k] = __ldcg(p.part_ml + x);
+                    if (!in) ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) y[k][j] = __ldcg(reinterpret_cast<const float2 *>(p.part_o + x * D + lane * V) + j);
+                }
+                const float Mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M), ref = Mn == -INFINITY ? 0.f : Mn;
+                const float f0 = ex2(M - ref);
+                M = Mn;
+                L *= f0;
+#pragma unroll
+                for (int j = 0; j < V; ++j) a[j] *= f0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = ex2(ml[k].x - ref);
+                    L += f * ml[k].y;
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        a[2 * j] += f * y[k][j].x;
+                        a[2 * j + 1] += f * y[k][j].y;
+                    }
                 }
             }
             const float inv = M == -INFINITY ? 0.f : 1.f / L;
