@@ -48,11 +48,18 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
     return KDA_OK;
 }
 
-// Rows of one sequence and key head (new tokens times query heads) up to which the kernel of
-// few rows runs.
-constexpr int kFewRows = 16;
+// The kernel of few rows runs up to kFewRows rows of a sequence and key head (new tokens times
+// query heads), and where there are at most kFewUnits 64-key units a CTA, as many as the sizes
+// allow; the chunk kernel otherwise.  Few rows are bound by memory and want many CTAs' loads; the
+// chunk kernel's tiles are 128 rows whatever there is, and its plan, pieces and join take some 15 us.
+// Measured (few rows / chunk kernel, us), 4 key heads of 128, 64 sequences of 128 to 8192 keys: 24
+// rows 83 / 90, 32 rows 81 / 93, 64 rows 143 / 99; of 64: 32 rows 52 / 82.  By units a CTA: 5 (256
+// tokens over 1024, 8 heads of 64) 20 / 35, 8 (100 over 3000, 2 of 128) 26 / 40, 9 and 10: 37 / 32
+// and 23 / 24, 17 (16 chunks of 16 over 500) 30 / 27, 28 (512 over 512, 8 of 128) 50 / 30.
+constexpr int kFewRows = 32, kFewUnits = 9;
 
-// Keys of a full table up to which the kernel of few rows takes items whole.
+// Keys of a full table up to which the kernel of few rows takes items whole: one launch, no join
+// (one token over 257 keys, 4 heads of 64: 7.7 us from 8.9, and a launch less for the host).
 constexpr int kWholeKeys = 512;
 
 struct AttnPlan {
@@ -66,7 +73,13 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
     const int G = Hq / Hkv;
     if (max_q > total_q) max_q = total_q;
     a.sms = kda::host_num_sms(device());
-    a.chunk = (long long)max_q * G > kFewRows && kda::paged_chunk_pages(page_size);
+    const int few = kda::paged_rows_tile();
+    // units that there can be: every sequence's tiles, each over a full table
+    const long long seqs = N < total_q ? N : total_q;
+    const long long tiles = ((long long)total_q * G / few + seqs) * Hkv, span = ((long long)P * page_size + 63) / 64;
+    const long long top = (long long)a.sms * kda::paged_rows_ctas_per_sm(d);
+    a.chunk = (long long)max_q * G > kFewRows && (double)tiles * span > (double)(kFewUnits * top) &&
+              kda::paged_chunk_pages(page_size);
     long long rows;
     if (a.chunk) {
         a.tile = kda::paged_chunk_tile();
@@ -75,16 +88,10 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
         a.off_entries = 256 + up256(3 * (size_t)N * sizeof(int)) + up256((size_t)a.lim.pieces * kda::paged_chunk_piece_bytes());
         rows = a.lim.rows;
     } else {
-        a.tile = kda::paged_rows_tile();
-        // units that there can be: every sequence's tiles, each over a full table
-        const long long seqs = N < total_q ? N : total_q;
-        const long long tiles = (long long)total_q * G / a.tile + seqs;
-        const long long span = ((long long)P * page_size + 63) / 64;
-        const long long top = (long long)a.sms * kda::paged_rows_ctas_per_sm(d);
+        a.tile = few;
         a.whole = (long long)P * page_size <= kWholeKeys;
         a.ctas = (int)top;
-        if (a.whole) a.ctas = (int)(tiles * Hkv < top ? tiles * Hkv : top);
-        else if (tiles < top && tiles * Hkv < top && tiles * Hkv * span < top) a.ctas = (int)(tiles * Hkv * span);
+        if (tiles < top && (a.whole || tiles * span < top)) a.ctas = (int)(a.whole ? tiles : tiles * span);
         a.entries = a.whole ? 0 : a.ctas;
         rows = a.whole ? 0 : (long long)kda::paged_rows_slots(a.ctas) * a.tile;
     }

@@ -9,14 +9,15 @@ NAN16 = float("nan")
 
 
 def make(nq, ln, Hq, Hkv, d, ps, *, dtype=torch.bfloat16, layout="tokens", seed=0, spare=3, extra_rows=0, pad_q=0,
-         wide=False, permute=False, poison=True, q_scale=1.0):
+         wide=False, permute=False, poison=True, q_scale=1.0, span=0):
     """A batch of len(nq) sequences.  Every place of the pages that no token holds is NaN when
-    `poison`; the new tokens' places hold NaN too until the call writes them."""
+    `poison`; the new tokens' places hold NaN too until the call writes them.  The table has room for
+    `span` keys a row at least: the sizes are what the choice of kernel goes by."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     r = np.random.default_rng(seed)
     N, R = len(nq), len(nq) + extra_rows
     held = [-(-n // ps) for n in ln]
-    P = max(1, max(held)) + r.integers(0, 3)
+    P = max(1, max(held), -(-span // ps)) + int(r.integers(0, 3))
     pages = sum(held) + spare
     ids = r.permutation(pages)
     rows = r.permutation(R)[:N] if permute else np.arange(N)

@@ -49,7 +49,8 @@ def test_no_tokens_need_nothing(lib):
     assert kda.paged_attn_workspace_bytes(2, 0, 0, 8, 2, 64, 16, 4) == 0
     assert kda.paged_attn_workspace_bytes(2, 5, 4, 8, 2, 96, 16, 4) == 0
     assert kda.paged_attn_workspace_bytes(2, 5, 4, 8, 2, 64, 16, 40) > 0
-    assert kda.paged_attn_workspace_bytes(2, 50, 48, 8, 2, 64, 16, 4) > 0
+    assert kda.paged_attn_workspace_bytes(2, 50, 48, 8, 2, 64, 16, 4000) > 0
+    assert kda.paged_attn_workspace_bytes(2, 50, 48, 8, 2, 64, 16, 4) == 0  # short caches are not split
 
 
 def reserve(lib, table=A, length=A, ref=A, rows=A, new=A, n=2, info=None, R=4, P=4, pages=9, ps=16):

@@ -83,33 +83,37 @@ CHUNKS = [
 ]
 
 
+LONG = 1 << 18  # keys that a table has room for: past 32 rows the chunk kernel runs
+
+
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", TOKENS + FEW + CHUNKS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
-def test_against_64_bits(nq, ln, Hq, Hkv, d, ps, dtype):
-    run(make(nq, ln, Hq, Hkv, d, ps, dtype=dtype, seed=len(nq) + d))
+@pytest.mark.parametrize("span", [0, LONG], ids=["short", "long"])
+def test_against_64_bits(nq, ln, Hq, Hkv, d, ps, dtype, span):
+    run(make(nq, ln, Hq, Hkv, d, ps, dtype=dtype, seed=len(nq) + d, span=span))
 
 
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[5], FEW[1], CHUNKS[2], CHUNKS[7]])
 @pytest.mark.parametrize("layout", ["heads", "pair"])
 def test_layouts_slices_and_rows(nq, ln, Hq, Hkv, d, ps, layout):
-    c = make(nq, ln, Hq, Hkv, d, ps, layout=layout, wide=True, permute=True, extra_rows=3, pad_q=5, seed=9)
+    c = make(nq, ln, Hq, Hkv, d, ps, layout=layout, wide=True, permute=True, extra_rows=3, pad_q=5, seed=9, span=LONG)
     run(c)
 
 
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[5], FEW[3], CHUNKS[1], CHUNKS[8]])
 def test_cache_that_holds_the_new_tokens(nq, ln, Hq, Hkv, d, ps):
-    run(make(nq, ln, Hq, Hkv, d, ps, seed=4), append=False)
+    run(make(nq, ln, Hq, Hkv, d, ps, seed=4, span=LONG), append=False)
 
 
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[5], CHUNKS[2], CHUNKS[7]])
 def test_large_scores(nq, ln, Hq, Hkv, d, ps):
     # scores with a standard deviation of 12: the running maximum moves far and often
-    run(make(nq, ln, Hq, Hkv, d, ps, q_scale=12.0, seed=5))
+    run(make(nq, ln, Hq, Hkv, d, ps, q_scale=12.0, seed=5, span=LONG))
 
 
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[5], FEW[3], CHUNKS[5], CHUNKS[7]])
 def test_same_bits_again(nq, ln, Hq, Hkv, d, ps):
-    c = make(nq, ln, Hq, Hkv, d, ps, seed=6)
+    c = make(nq, ln, Hq, Hkv, d, ps, seed=6, span=LONG)
     a = call(c)
     for _ in range(3):
         b = call(c)
@@ -119,7 +123,7 @@ def test_same_bits_again(nq, ln, Hq, Hkv, d, ps):
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[8], CHUNKS[7]])
 def test_padded_batch(nq, ln, Hq, Hkv, d, ps):
     """Sequences of no tokens, as a captured graph pads its batch with, change nothing."""
-    c = make(nq, ln, Hq, Hkv, d, ps, seed=7)
+    c = make(nq, ln, Hq, Hkv, d, ps, seed=7, span=LONG)
     a = call(c)
     e = dict(c)
     e["cu"] = torch.cat([c["cu"], c["cu"][-1:].repeat(9)])
@@ -132,16 +136,10 @@ def test_padded_batch(nq, ln, Hq, Hkv, d, ps):
     assert ((a[0].double() - o).abs() <= tol).all()
 
 
-def grow(c, by):
-    """The same batch some tokens later (same new-token counts)."""
-    ln = [x + by for x in c["ln"]]
-    return make(c["nq"], ln, c["q"].shape[1], c["kp"].shape[2], c["q"].shape[2], c["ps"], seed=31 + by)
-
-
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [([1] * 4, [9, 70, 300, 33], 8, 2, 128, 16), ([60, 2], [200, 90], 8, 2, 64, 16)])
 def test_captured_and_replayed(nq, ln, Hq, Hkv, d, ps):
     """One graph, replayed for other lengths, tables and contents; two graphs in flight at once."""
-    big = make(nq, [x + 500 for x in ln], Hq, Hkv, d, ps, seed=1)
+    big = make(nq, [x + 500 for x in ln], Hq, Hkv, d, ps, seed=1, span=LONG)
     keys = ("q", "kn", "vn", "kp", "vp", "cu", "table", "length")
 
     def load_into(h, c):
@@ -212,7 +210,7 @@ BAD = ["page", "negative page", "length", "negative length", "row", "cu order", 
 @pytest.mark.parametrize("nq,ln", [([1, 1, 2], [100, 40, 7]), ([40, 3, 90], [100, 40, 200])], ids=["few", "chunk"])
 def test_bad_numbers_are_reported(what, nq, ln):
     """Nothing outside the buffers is touched: the pages' and outputs' neighbours keep their bits."""
-    c = make(nq, ln, 8, 2, 64, 16, seed=8, permute=True, poison=False)
+    c = make(nq, ln, 8, 2, 64, 16, seed=8, permute=True, poison=False, span=LONG)
     kb = torch.full((c["kp"].shape[0] + 2, *c["kp"].shape[1:]), 3.0, dtype=c["q"].dtype, device="cuda")
     vb = kb.clone()
     kb[1:-1], vb[1:-1] = c["kp"], c["vp"]
@@ -245,7 +243,7 @@ def test_bad_numbers_are_reported(what, nq, ln):
 @pytest.mark.parametrize("nq,ln", [([300, 2], [900, 70]), ([1, 1], [9000, 70])], ids=["chunk", "few"])
 def test_waits_that_give_up_are_reported(nq, ln):
     """With no patience at all the chunk kernel's waits run out; the call ends, says so, and the next one works."""
-    c = make(nq, ln, 8, 2, 128, 64, seed=2)
+    c = make(nq, ln, 8, 2, 128, 64, seed=2, span=LONG)
     kp, vp = appended(c)
     try:
         kda.set_wait_limit(1)
