@@ -187,7 +187,7 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
                    void *workspace, size_t workspace_bytes, void *stream) {
     if (const int st = attn_sizes(N, total_q, max_q, Hq, Hkv, d, page_size, P); st != KDA_OK) return st;
     if (num_pages < 1 || R < 1 || (rows == nullptr && R < N)) return KDA_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale > 3.0e38f) return KDA_ERR_INVALID_ARG;  // also rejects NaN
+    if (!(scale > 0.f) || scale > 1.0e30f) return KDA_ERR_INVALID_ARG;  // also rejects NaN
     if (dtype != KDA_BF16 && dtype != KDA_FP16) return KDA_ERR_UNSUPPORTED;
     if (!cu_q || !page_table || !length || !k_pages || !v_pages || (k_new == nullptr) != (v_new == nullptr))
         return KDA_ERR_INVALID_ARG;

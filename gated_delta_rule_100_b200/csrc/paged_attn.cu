@@ -297,8 +297,9 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 mx = fmaxf(mx, m[e]);
-                const float ref = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every weight is 2^-inf = 0
-                f[e] = ex2(m[e] - ref);
+                const float top = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every weight is 2^-inf = 0
+                const float ref = top - weight_shift<BF>();
+                f[e] = ex2(m[e] - top);
                 m[e] = mx;
                 float sum = 0.f;
 #pragma unroll
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
         for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            m[e] -= weight_shift<BF>();
             if (t4 == 0) s_ml[warp][g8 + 8 * e] = make_float2(m[e], l[e]);
         }
         __syncthreads();

@@ -13,10 +13,10 @@
 //   tile's warps form weights, the tensor cores work on the other tile.
 // - one warp issues every product, one loads pages by TMA into a ring (key and
 //   value tiles of 128 keys in turn), eight own a row per thread.
-// - the sums stay in TMEM.  They are rescaled only when a row's maximum grows by
-//   more than 2^8 over the one in use (weights up to 2^8 lose nothing: 16-bit
-//   rounding is relative and the sums are fp32), so after the first keys hardly
-//   ever.
+// - the sums stay in TMEM.  They are rescaled only when a row's weights outgrow
+//   the reference in use, the maximum of its first keys as a rule (weights of
+//   2^7 lose nothing: 16-bit rounding is relative and the sums are fp32), so
+//   after the first keys hardly ever.
 // - the rows of masked keys behind the sequence's end are zeroed in the last
 //   value tile: a page holds anything there, and 0 x NaN is NaN.
 //
@@ -91,8 +91,8 @@ constexpr int CK_CAND = 16;
 __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64, 128, 256};
 
 __device__ void ck_plan(const ChunkParams &c, int d) {
-    __shared__ unsigned long long s_w;
-    __shared__ unsigned s_wa, s_a, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // pieces and eighths of rows of one key head
+    __shared__ unsigned long long s_w, s_wa, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // of one key head; rows in eights
+    __shared__ unsigned s_a;
     __shared__ int s_max, s_ma, s_items, s_step, s_phi, s_entries, s_part, s_sum[33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
@@ -132,14 +132,15 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     auto whole = [&](int tiles, int phi) { return phi ? (int)(tiles * phi1) : 0; };
     {   // a lane a candidate; few sequences share the warps among their tiles
         const int q = lane / CK_CAND, split = max(1, warps / p.N);
-        const float inv = 1.f / ((s_max + ck_div[lane % CK_CAND] - 1) / ck_div[lane % CK_CAND]);
-        unsigned pieces = 0, rows8 = 0, wa = 0, na = 0;
+        const int step = (s_max + ck_div[lane % CK_CAND] - 1) / ck_div[lane % CK_CAND];
+        unsigned long long pieces = 0, rows8 = 0, wa = 0;
+        unsigned na = 0;
         int ma = 0;
         for (int v = warp; v < p.N * split; v += warps) {
             const PagedSeq s = paged_seq(p, v % p.N, false);
             const int tiles = ck_tiles(s, G), a = whole(tiles, 1);
             for (int t = v / p.N; t < tiles; t += split) {
-                const int k = ck_keys(s, G, t), ns = (int)ceilf(k * inv - 1e-3f);  // near enough for the choice
+                const int k = ck_keys(s, G, t), ns = (k + step - 1) / step;
                 const bool in_a = tiles - 1 - t < a;
                 if (in_a) { wa += k; ++na; ma = max(ma, k); }
                 if (!(q && in_a)) {
@@ -166,7 +167,9 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
         float cost = ka * ta + (pb > early ? ceilf((pb - early) / S) * tb : 0.f);
         cost = fmaxf(cost, max(pa > 0.f ? s_ma : 0, pb > 0.f ? step : 0) + 3.f);  // no less than the longest
         if (R > 0.f) cost += 3.f + R * d * 8.f * 1.2e-7f;
-        if (lane > 0 && (pa + pb > c.max_pieces || R > c.max_rows)) cost = 3.0e38f;
+        // what the workspace has no room for is out (not the uncut items, which it always has room for)
+        const unsigned long long np = (s_pieces[lane] + (q ? s_a : 0u)) * p.Hkv, nr = s_rows8[lane] * 8ull * p.Hkv;
+        if (lane > 0 && (np > (unsigned long long)c.max_pieces || nr > (unsigned long long)c.max_rows)) cost = 3.0e38f;
         float best = cost;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -381,30 +384,31 @@ __device__ __forceinline__ bool elect_lane() {
     return r != 0;
 }
 
-// 2^x without the exponential unit, for x = s sc - ref: y = (x + 120) / 128 in one
-// operation that also holds it in [0, 1] (x in [-120, 8]); x = n + r with n the
-// nearest integer (128 y - 120 added to 1.5 2^23, whose last place is 1, leaves n
-// in the low bits) and r in [-1/2, 1/2]; 2^r by the polynomial of degree 4 with
+// 2^x without the exponential unit, for x = s sc - ref: y = (x + LOW) / 128 in one
+// operation that also holds it in [0, 1] (x in [-LOW, 128 - LOW]); x = n + r with n
+// the nearest integer (128 y - LOW added to 1.5 2^23, whose last place is 1, leaves
+// n in the low bits) and r in [-1/2, 1/2]; 2^r by the polynomial of degree 4 with
 // the least largest relative error there, 2.7e-6 (a least-squares fit with its
 // weights moved to the error's peaks); n added to the exponent.  y's last place
-// is another 2.6e-6; a weight's 16-bit rounding is 100 times both.  A score far
-// below the maximum weighs 2^-120 and not 0: not for masked keys.
-struct PolyScale {
+// is another 2.6e-6; a weight's 16-bit rounding is 50 times both or more.  A score
+// far below the maximum weighs 2^-LOW and not 0: not for masked keys.
+template <bool BF>
+struct Poly {
+    static constexpr float LOW = BF ? 120.f : 112.f, SHIFT = 12582912.f - LOW;
     float a, b;  // y = s a + b
+    __device__ __forceinline__ Poly(float sc, float ref) : a(sc * 0.0078125f), b((LOW - ref) * 0.0078125f) {}
+    __device__ __forceinline__ float operator()(float s) const {
+        float y;
+        asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(s), "f"(a), "f"(b));
+        const float t = fmaf(y, 128.f, SHIFT);
+        const float r = fmaf(y, 128.f, SHIFT - t);
+        float q = fmaf(r, 0.0095701003447f, 0.0559178590775f);
+        q = fmaf(q, r, 0.2402474433184f);
+        q = fmaf(q, r, 0.6931217908859f);
+        q = fmaf(q, r, 0.9999992847443f);
+        return __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));
+    }
 };
-__device__ __forceinline__ PolyScale poly_scale(float sc, float ref) { return {sc * 0.0078125f, (120.f - ref) * 0.0078125f}; }
-__device__ __forceinline__ float exp2_poly(float s, const PolyScale &k) {
-    constexpr float shift = 12582912.f - 120.f;
-    float y;
-    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(s), "f"(k.a), "f"(k.b));
-    const float t = fmaf(y, 128.f, shift);
-    const float r = fmaf(y, 128.f, shift - t);
-    float q = fmaf(r, 0.0095701003447f, 0.0559178590775f);
-    q = fmaf(q, r, 0.2402474433184f);
-    q = fmaf(q, r, 0.6931217908859f);
-    q = fmaf(q, r, 0.9999992847443f);
-    return __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));
-}
 
 // Weights 2^(x sc - ref) of a row's 64 scores as 16-bit pairs, and their sum
 // before the rounding.  MIX: one of eight by the polynomial, which makes up for
@@ -412,13 +416,13 @@ __device__ __forceinline__ float exp2_poly(float s, const PolyScale &k) {
 // pipe's share beside it); it has no 0 for masked keys.
 template <bool BF, bool MIX>
 __device__ __forceinline__ float ck_weights(const uint32_t (&x)[CK_STEP], uint32_t (&y)[CK_STEP / 2], float sc, float ref) {
-    const PolyScale ps = poly_scale(sc, ref);
+    const Poly<BF> poly(sc, ref);
     float l[4] = {};
 #pragma unroll
     for (int k = 0; k < CK_STEP; k += 2) {
         const float u = __uint_as_float(x[k]), v = __uint_as_float(x[k + 1]);
         const float a = ex2(fmaf(u, sc, -ref));
-        const float b = MIX && k % 8 == 0 ? exp2_poly(v, ps) : ex2(fmaf(v, sc, -ref));
+        const float b = MIX && k % 8 == 0 ? poly(v) : ex2(fmaf(v, sc, -ref));
         l[k & 2] += a;
         l[(k & 2) + 1] += b;
         y[k / 2] = pack16x2<BF>(a, b);
@@ -681,6 +685,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int w = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + S::TM_S + w * 128, to = tmem + lanes + S::TM_O + w * D;
+        // weights are shifted up by SH; sums of 64 of them may reach 2^7 times the reference's own
+        constexpr float SH = weight_shift<BF>(), MOST = BF ? 128.f : 32768.f;
         uint32_t s_phase = 0, h_phase = 0;  // completions of this tile's B_S, B_HALF
         bool ok = true;
         for (uint32_t kp = 0; ok; ++kp) {
@@ -734,7 +740,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // both halves' weights lie over the first half's scores, which are read by then
                 const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
                 // Unmasked keys: the weights with the reference there is, looked at afterwards, so that no
-                // maximum stands between scores and weights.  A sum of the 64 up to 2^7 keeps every weight
+                // maximum stands between scores and weights.  A sum of the 64 up to MOST keeps every weight
                 // there too; past it the step is done again below, from the scores still in TMEM.
                 bool done = false;
                 float sum;
@@ -743,8 +749,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     tm_ld32(sb, x);
                     tm_ld32(sb + 32, x + 32);
                     tmem_wait_ld();
-                    sum = ck_weights<BF, true>(x, y, sc, m * sc);
-                    done = !__any_sync(0xffffffffu, sum > 128.f);
+                    sum = ck_weights<BF, true>(x, y, sc, m * sc - SH);
+                    done = !__any_sync(0xffffffffu, sum > MOST);
                     if (done) tm_st32(pb, y);
                 }
                 if (!done) {
@@ -783,7 +789,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         }
                     }
                     if (unset) unset = __any_sync(0xffffffffu, m == -INFINITY);
-                    sum = ck_weights<BF, false>(x, y, sc, m == -INFINITY ? 0.f : m * sc);
+                    sum = ck_weights<BF, false>(x, y, sc, (m == -INFINITY ? 0.f : m * sc) - SH);
                     tm_st32(pb, y);
                 }
                 l += sum;
@@ -826,9 +832,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     }
                 }
                 if (real) {
-                    if (!whole) p.part_ml[pc.part_row + row] = make_float2(m == -INFINITY ? m : m * sc, l);
+                    if (!whole) p.part_ml[pc.part_row + row] = make_float2(m == -INFINITY ? m : m * sc - SH, l);
                     else if (p.lse != nullptr)
-                        p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = m == -INFINITY ? -INFINITY : m * sc * LN2 + logf(l);
+                        p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = m == -INFINITY ? -INFINITY : (m * sc - SH) * LN2 + logf(l);
                 }
                 tc_fence_before();
             }

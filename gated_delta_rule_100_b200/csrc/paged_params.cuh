@@ -11,7 +11,7 @@
 namespace kda {
 
 // One row's partial result over part of its keys: unnormalised sums against a
-// reference m (log2 units) and l = sum of 2^(x - m).  The first piece of a split
+// reference m (log2 units, the weights' shift taken off) and l = sum of 2^(x - m).  The first piece of a split
 // item has its rows from part row `head`, the `count` others from `next`,
 // `stride` rows apart.
 struct SplitEntry {
@@ -88,6 +88,15 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// Binary orders that a weight is shifted up by before it is rounded to 16 bits.
+// bf16 reaches as far as fp32.  fp16 has full precision down to 2^-14 only, and a
+// row whose first key outweighs the others (an attention sink) may have most of
+// its other keys below that: shifted, weights keep it down to 2^-22 of the
+// reference, with 2^7 left above it (as many orders up as the chunk kernel needs:
+// with 2^3 it moved references so often that a mixed batch took 110 us for 81).
+template <bool BF>
+__host__ __device__ constexpr float weight_shift() { return BF ? 0.f : 8.f; }
 
 constexpr float LN2 = 0.69314718055994531f;
 

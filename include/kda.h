@@ -410,7 +410,7 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  *   length     : int32 [R]      tokens of a row WITH the new ones
  *   rows       : int32 [N] the sequences' rows of page_table and length, or
  *                NULL for rows 0 .. N - 1
- *   scale      : > 0, finite (commonly d^-0.5)
+ *   scale      : > 0, at most 1e30 (commonly d^-0.5)
  *   out        : [total_q, Hq, d]
  *   lse        : fp32 [total_q, Hq] log of the sum of exp(scale q.k), or NULL
  *   max_q      : no sequence has more new tokens than this
@@ -629,7 +629,7 @@ KDA_API int kda_debug_kernel_launches(int *kind, long long *start_ns, long long 
  * points, 102 the packed-batch prefill, the raw-input (fused gate prologue)
  * entry points, the backward pass and the exact-path and two-level test
  * hooks, 103 the host-buffer prefill and the per-launch timing list, 104 the
- * block-reference test hook. */
+ * block-reference test hook and the paged cache. */
 KDA_API int kda_abi_version(void);
 
 #ifdef __cplusplus

@@ -86,8 +86,14 @@ def attention64(c, kp, vp):
     u sum p_j |v_j| after the division), the result once more (u |o|).  A score's products are
     exact in 32 bits, their d sums lose at most 2^-23 of sum |q||k| each (tensor cores may
     truncate), scaling and the exponential a few 2^-23 of the score and of the weight; the sums
-    over keys lose at most 2^-23 a key."""
+    over keys lose at most 2^-23 a key.
+
+    fp16's steps stop shrinking at 2^-14, where half of one is 2^-25.  Weights are rounded as
+    2^8 times their ratio to a reference that is no larger than the row's largest, so a
+    ratio below 2^-22 is off by at most 2^-25 / 2^8 = 2^-33: sum |v_j| times that, over the
+    sum of the ratios, e^(z - max), joins the bound."""
     u = torch.finfo(c["q"].dtype).eps / 2
+    tiny = 2.0 ** -33 if c["q"].dtype == torch.float16 else 0.0
     q = c["q"].double()
     total, Hq, d = q.shape
     Hkv = kp.shape[2]
@@ -112,10 +118,12 @@ def attention64(c, kp, vp):
             p = torch.where(see, torch.exp(s - torch.where(some, z, 0.0)[..., None]), 0.0)
             o = torch.einsum("htk,khd->thd", p, V)
             a = torch.einsum("htk,khd->thd", p, V.abs())
+            top = torch.where(some, torch.exp(s.amax(-1) - z), 0.0)
+            low = tiny * top.T[..., None] * torch.einsum("htk,khd->thd", see.double().expand(Hq, t, L), V.abs())
             ds = 2.0 ** -23 * (d + 4) * torch.where(see, mag, 0.0).amax(-1) + 2.0 ** -21  # of the scores, [h, t]
             rest = 2 * ds + 2.0 ** -23 * (L + 64)
             out[at: at + t] = o
-            tol[at: at + t] = u * a + u * (o.abs() + u * a) + rest.T[..., None] * a + 2.0 ** -25
+            tol[at: at + t] = u * a + low + u * (o.abs() + u * a) + rest.T[..., None] * a + 2.0 ** -25
             lse[at: at + t] = z.T
             ltol[at: at + t] = (ds + 2.0 ** -23 * (L + 64)).T + 2.0 ** -22 * torch.where(some, z.abs(), 0.0).T
         at += t

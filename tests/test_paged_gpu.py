@@ -80,6 +80,8 @@ CHUNKS = [
     ([40, 1, 90], [1040, 2000, 91], 12, 4, 128, 24),  # a page size that is no power of two
     ([50], [50], 5, 1, 64, 9),
     ([1000], [1000], 7, 1, 128, 256),
+    ([90], [1000], 2, 1, 128, 8),
+    ([200, 1], [777, 800], 4, 2, 64, 384),
 ]
 
 
@@ -109,6 +111,27 @@ def test_cache_that_holds_the_new_tokens(nq, ln, Hq, Hkv, d, ps):
 def test_large_scores(nq, ln, Hq, Hkv, d, ps):
     # scores with a standard deviation of 12: the running maximum moves far and often
     run(make(nq, ln, Hq, Hkv, d, ps, q_scale=12.0, seed=5, span=LONG))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq,ln", [([1, 1], [9000, 300]), ([100], [9000])], ids=["few", "chunk"])
+@pytest.mark.parametrize("gap", [12.0, 20.0])
+def test_sink(nq, ln, dtype, gap):
+    """One key outweighs every other by 2^17 (2^29): what thousands of the others add up to is kept, though each is far
+    below fp16's smallest normal number."""
+    c = make(nq, ln, 2, 1, 64, 16, dtype=dtype, seed=3, span=LONG, poison=False)
+    for t in (c["q"], c["kp"], c["kn"]):
+        t.zero_()
+    c["q"][..., 0] = 8.0
+    for n in range(len(nq)):
+        c["kp"][int(c["table"][c["row_of"][n], 0]), 0, :, 0] = gap  # scale 1/8: a score of `gap`
+    c["vp"].abs_().add_(1.0)
+    c["vn"].abs_().add_(1.0)
+    for n in range(len(nq)):
+        c["vp"][int(c["table"][c["row_of"][n], 0]), 0] = 0.0  # the sink's own value
+    kp, vp = appended(c)
+    out, lse = call(c)
+    check(c, out, lse, kp, vp)
 
 
 @pytest.mark.parametrize("nq,ln,Hq,Hkv,d,ps", [TOKENS[5], FEW[3], CHUNKS[5], CHUNKS[7]])
