@@ -24,7 +24,7 @@ cudaError_t launch_pages_free(const PagesParams &p, int sms, cudaStream_t stream
 cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t stream);
 int compact_blocks(int num_pages);
 cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t stream);
-cudaError_t launch_pages_copy(const PoolParams &p, bool check, int sms, cudaStream_t stream);
+cudaError_t launch_pages_copy(PoolParams p, bool check, int sms, cudaStream_t stream);
 }  // namespace kda
 
 namespace {

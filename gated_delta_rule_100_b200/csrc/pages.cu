@@ -370,17 +370,22 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const PagesParams p)
 
 // ------------------------------------------------------------------- copy ----
 // pool[o][dst[i]] = pool[o][src[i]] for every pair and outer index, in units of
-// at most 16 KB: 256 threads, four 16-byte loads in flight each, then four
-// stores, and enough blocks on an SM to cover the latency.  A pair whose
-// destination the list names elsewhere too (as a destination or as a source) is
-// not copied: the others read what was there before the call.
-constexpr int COPY_THREADS = 256, COPY_UNIT = 16384;
+// at most 64 KB: 256 threads with sixteen 16-byte loads in flight each, then the
+// stores.  128 pages of 32 x 131 KB take 173 us (6.2 TB/s moved, 95 % of the
+// card's copy rate), from 188, 184 and 176 us with units of 8, 16 and 32 KB; cache
+// hints for data read and written once (187 us at 16 KB) and half the blocks (187
+// us at 32 KB) were slower.  Where that is more than an SM's share units are
+// halved, to 8 KB at least (a 256 KB state: 2.9 us from 3.7; 33 MB in units of 8 KB
+// took 9 us longer than in 64).  A pair whose destination the list names elsewhere too
+// (as a destination or as a source) is not copied: the others read what was there
+// before the call.
+constexpr int COPY_THREADS = 256, COPY_VECS = 16, COPY_UNIT = COPY_THREADS * COPY_VECS * 16;
 
 template <bool CHECK>
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolParams p) {
     wait_for_primary();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
-    const long long per_page = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT, per_pair = per_page * p.outer;
+    const long long per_page = (p.page_bytes + p.unit - 1) / p.unit, per_pair = per_page * p.outer;
     const long long units = n * per_pair;
     const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
     int pair = -1, from = 0, to = 0;
@@ -404,19 +409,24 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolPara
             if (bad && threadIdx.x == 0) report(p.st, DEV_BAD_ARG);
         }
         if (!ok || from == to) continue;
-        const long long in_pair = u % per_pair, o = in_pair / per_page, at = (in_pair % per_page) * COPY_UNIT;
-        const int vecs = (int)(min((long long)COPY_UNIT, p.page_bytes - at) / 16);
+        const long long in_pair = u % per_pair, o = in_pair / per_page, at = (in_pair % per_page) * p.unit;
+        const int vecs = (int)(min((long long)p.unit, p.page_bytes - at) / 16);
         const uint8_t *base = p.pool + o * p.outer_stride + at;
         const uint4 *a = reinterpret_cast<const uint4 *>(base + from * p.page_stride);
         uint4 *b = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(base) + to * p.page_stride);
+        uint4 x[COPY_VECS];
         if (vecs == COPY_UNIT / 16) {
-            uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = __ldcs(a + k * COPY_THREADS + threadIdx.x);
+            for (int k = 0; k < COPY_VECS; ++k) x[k] = a[k * COPY_THREADS + threadIdx.x];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) __stcs(b + k * COPY_THREADS + threadIdx.x, x[k]);
+            for (int k = 0; k < COPY_VECS; ++k) b[k * COPY_THREADS + threadIdx.x] = x[k];
         } else {
-            for (int k = threadIdx.x; k < vecs; k += COPY_THREADS) __stcs(b + k, __ldcs(a + k));
+#pragma unroll
+            for (int k = 0; k < COPY_VECS; ++k)
+                if (k * COPY_THREADS + threadIdx.x < vecs) x[k] = a[k * COPY_THREADS + threadIdx.x];
+#pragma unroll
+            for (int k = 0; k < COPY_VECS; ++k)
+                if (k * COPY_THREADS + threadIdx.x < vecs) b[k * COPY_THREADS + threadIdx.x] = x[k];
         }
     }
 }
@@ -463,8 +473,10 @@ cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t str
     const long long grid = want > want2 ? want : want2;
     return launch_behind(compact_apply_kernel, dim3((unsigned)(grid < top ? grid : top)), 256, 0, stream, p);
 }
-cudaError_t launch_pages_copy(const PoolParams &p, bool check, int sms, cudaStream_t stream) {
-    const long long units = (p.page_bytes + COPY_UNIT - 1) / COPY_UNIT * p.outer * p.n, top = 8LL * sms;
+cudaError_t launch_pages_copy(PoolParams p, bool check, int sms, cudaStream_t stream) {
+    const double each = (double)p.page_bytes * p.outer * p.n / sms;  // bytes an SM
+    for (p.unit = COPY_UNIT; p.unit > COPY_UNIT / 8 && p.unit > each; p.unit /= 2) {}
+    const long long units = (p.page_bytes + p.unit - 1) / p.unit * p.outer * p.n, top = 8LL * sms;
     return launch_behind(check ? pages_copy_kernel<true> : pages_copy_kernel<false>, dim3((unsigned)(units < top ? units : top)),
                          COPY_THREADS, 0, stream, p);
 }

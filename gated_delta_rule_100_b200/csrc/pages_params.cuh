@@ -25,7 +25,7 @@ struct PoolParams {
     uint8_t *pool;
     const int *src, *dst, *count;    // count: pairs, on the device, or NULL
     long long outer, outer_stride, page_stride, page_bytes;
-    int num_pages, n;
+    int num_pages, n, unit;          // unit: bytes that a block copies at a time
     DeviceStatus st;
 };
 
