@@ -547,9 +547,10 @@ cudaError_t launch_pages_grant(const PagesParams &p, bool fork, cudaStream_t str
     return launch_behind(k, dim3(PG_CLUSTER), PG_THREADS, smem, stream, p);
 }
 int compact_blocks(int num_pages) { return (num_pages + CP_BLOCK - 1) / CP_BLOCK; }
-// Pages and table entries up to which one launch compacts (a 300-page cache: 9.2 us with its pool from 10.6, and
-// two launches less for the host; 8 SMs would take longer than the rest saves past some 100,000).
-constexpr int COMPACT_SMALL = 65536;
+// Pages and table entries up to which one launch compacts: one launch / three, for 300 pages and 1024 entries
+// 5.9 / 6.8 us, 16,384 of each 9.2 / 8.7 us, 65,536 of each 17.0 / 9.7 us, and for the host two launches
+// (4 us of 20) less.
+constexpr int COMPACT_SMALL = 16384;
 cudaError_t launch_pages_compact(const PagesParams &p, int sms, cudaStream_t stream) {
     if (p.num_pages <= COMPACT_SMALL && (long long)p.R * p.P <= COMPACT_SMALL)
         return launch_behind(compact_small_kernel, dim3(PG_CLUSTER), PG_THREADS, 0, stream, p);

@@ -682,7 +682,13 @@ def _pool(t, num_pages, dev):
     es = t.element_size()
     page = want * es
     ps = st[1] * es if num_pages > 1 else page
-    return t.data_ptr(), shape[0], st[0] * es if shape[0] > 1 else ps * num_pages, ps, page
+    p, outer, os = t.data_ptr(), shape[0], st[0] * es if shape[0] > 1 else ps * num_pages
+    if (p | os | ps | page) & 15 or page < 1 or ps < page or os < page or outer > 1 << 24:
+        # refused here, before a call that changes the table has run
+        rc = load().kda_pages_copy(p, outer, os, ps, page, num_pages, None, None, 0, None)
+        if rc != KDA_OK:
+            raise KdaError(rc, "kda_pages_copy")
+    return p, outer, os, ps, page
 
 
 def pages_reserve(table, length, ref, rows, new_length, page_size, *, info=None, stream=None):

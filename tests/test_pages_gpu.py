@@ -283,6 +283,43 @@ def test_compact_moves_the_pools(R, P, pages, ps):
     assert torch.equal(a, wa) and torch.equal(b, wb)
 
 
+def test_compact_moves_the_pools_of_a_large_cache():
+    """More pages than one launch compacts."""
+    c = Cache(700, 100, 70001, 4)
+    r = np.random.default_rng(3)
+    t, ln, ref = c.cuda()
+    rows, new = np.arange(700), r.integers(300, 401, 700)
+    kda.pages_reserve(t, ln, ref, ints(*rows.tolist()), ints(*new.tolist()), 4)
+    c.reserve(rows, new)
+    gone = r.permutation(700)[:350]
+    kda.pages_free(t, ln, ref, ints(*gone.tolist()), 4)
+    c.free(gone)
+    a = torch.randint(0, 1 << 20, (2, 70001, 8), device="cuda", dtype=torch.int32)
+    want = a.clone()
+    kda.pages_compact(t, ln, ref, 4, pools=[a])
+    f, to = torch.tensor(c.compact(), device="cuda").T
+    want[:, to] = want[:, f]
+    c.same(t, ln, ref)
+    assert torch.equal(a, want) and kda.stream_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("bad", ["bytes", "pointer", "overlap"])
+def test_bad_pools_are_refused_before_the_table_changes(bad):
+    c = Cache(4, 4, 10, 8)
+    c.reserve([0, 1, 2], [30, 9, 4])
+    c.free([0])
+    good = torch.zeros((1, 10, 8), device="cuda")
+    pool = {"bytes": lambda: torch.zeros((2, 10, 3), device="cuda"), "pointer": lambda: torch.zeros(90, device="cuda")[1:81].view(1, 10, 8),
+            "overlap": lambda: good.expand(3, 10, 8)}[bad]()
+    t, ln, ref = c.cuda()
+    with pytest.raises(kda.KdaError):
+        kda.pages_fork(t, ln, ref, ints(1), ints(3), 8, pools=[good, pool])
+    with pytest.raises(kda.KdaError):
+        kda.pages_compact(t, ln, ref, 8, pools=[good, pool])
+    c.same(t, ln, ref)
+    assert kda.stream_status() == kda.KDA_OK
+
+
 def test_captured_page_calls():
     """reserve, fork with copies, free and compact in one graph, replayed on changed lists."""
     R, P, pages, ps = 16, 8, 120, 4
