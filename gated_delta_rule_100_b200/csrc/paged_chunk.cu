@@ -91,19 +91,20 @@ constexpr int CK_CAND = 16;
 __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64, 128, 256};
 
 __device__ void ck_plan(const ChunkParams &c, int d) {
-    __shared__ unsigned long long s_w, s_wa, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // of one key head; rows in eights
+    __shared__ unsigned long long s_w, s_wa, s_q, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // of one key head; rows in eights
     __shared__ unsigned s_a;
     __shared__ int s_max, s_ma, s_items, s_step, s_phi, s_entries, s_part, s_sum[33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
-    if (tid == 0) { s_w = 0; s_wa = s_a = 0; s_max = 1; s_ma = s_items = s_entries = s_part = 0; }
+    if (tid == 0) { s_w = s_q = 0; s_wa = s_a = 0; s_max = 1; s_ma = s_items = s_entries = s_part = 0; }
     if (tid < 2 * CK_CAND) s_pieces[tid] = s_rows8[tid] = 0;
     __syncthreads();
     // a warp a sequence, a lane a row tile
-    unsigned long long w = 0;
+    unsigned long long w = 0, tokens = 0;
     int mx = 1, items = 0;
     for (int n = warp; n < p.N; n += warps) {
         const PagedSeq s = paged_seq(p, n, lane == 0);
+        tokens += s.nq;
         for (int t = lane; t < ck_tiles(s, G); t += 32) {
             const int k = ck_keys(s, G, t);
             w += k;
@@ -122,10 +123,15 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     items = __reduce_add_sync(0xffffffffu, items);
     if (lane == 0 && items) {
         atomicAdd(&s_w, w);
+        atomicAdd(&s_q, tokens);
         atomicMax(&s_max, mx);
         atomicAdd(&s_items, items);
     }
     __syncthreads();
+    if (s_q > (unsigned long long)p.total_q) {  // sequences overlap, which was reported: more work than there is room for
+        if (tid == 0) c.head->pieces = c.head->ticket = c.head->entries = 0;
+        return;
+    }
     const long long all = (long long)s_items * p.Hkv;
     const float phi1 = (float)(all / c.sms * c.sms) / fmaxf((float)all, 1.f);
     // whole tiles of a sequence: ranks below, counted from the one with the most keys
@@ -249,13 +255,13 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
                         const int e = atomicAdd(&s_entries, 1);
                         if (e < c.max_entries && part + ns * r <= c.max_rows)
                             p.entries[e] = {n, h, t, part, part + r, ns - 1, r};
-                        else report(p.st, DEV_BAD_ARG);  // only where sequences overlap
+                        else report(p.st, DEV_BAD_ARG);  // only where cu_q or length change meanwhile
                     }
                     for (int j = 0; j < ns; ++j) {
                         const long long i = w1 ? (long long)c.base[n] + (long long)h * a + rank
                                           : j < full ? f0 + (long long)h * full_head + full_before + fi - full + j
                                                      : r0 + (long long)h * rest_head + rest_before + ri - 1;
-                        if (i >= c.max_pieces) { report(p.st, DEV_BAD_ARG); continue; }
+                        if ((unsigned long long)i >= (unsigned long long)c.max_pieces) { report(p.st, DEV_BAD_ARG); continue; }
                         const int kv0 = j * step, row = part < 0 ? -1 : part + j * r;
                         // a piece without room for its sums is left empty
                         const bool room = part < 0 || part + ns * r <= c.max_rows;
@@ -417,7 +423,7 @@ struct Poly {
 template <bool BF, bool MIX>
 __device__ __forceinline__ float ck_weights(const uint32_t (&x)[CK_STEP], uint32_t (&y)[CK_STEP / 2], float sc, float ref) {
     const Poly<BF> poly(sc, ref);
-    float l[4] = {};
+    float l[4] = {}, nan = 0.f;
 #pragma unroll
     for (int k = 0; k < CK_STEP; k += 2) {
         const float u = __uint_as_float(x[k]), v = __uint_as_float(x[k + 1]);
@@ -425,9 +431,11 @@ __device__ __forceinline__ float ck_weights(const uint32_t (&x)[CK_STEP], uint32
         const float b = MIX && k % 8 == 0 ? poly(v) : ex2(fmaf(v, sc, -ref));
         l[k & 2] += a;
         l[(k & 2) + 1] += b;
+        if (MIX && k % 8 == 0) asm("max.NaN.f32 %0, %0, %1;" : "+f"(nan) : "f"(v));  // which the polynomial's clamp drops
         y[k / 2] = pack16x2<BF>(a, b);
     }
-    return (l[0] + l[1]) + (l[2] + l[3]);
+    const float sum = (l[0] + l[1]) + (l[2] + l[3]);
+    return MIX && nan != nan ? nan : sum;
 }
 
 // The issuing lane's walk over a piece.  Its loop holds the steps of one key tile
@@ -801,7 +809,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // the sums, after the last product
             if (ok && (ok = wait_warp(S::B_S + w, (s_phase + nt) & 1))) {
                 tc_fence_after();
-                const ChunkPiece pc = c.pieces[at];  // read again_%=: the loop above needs the registers
+                const ChunkPiece pc = c.pieces[at];  // read again: the loop above needs the registers
                 const PagedSeq sq = pc.s;
                 const int row = w * CK_M + r, tok = (pc.t * CK_ROWS + row) / G, head = pc.h * G + (pc.t * CK_ROWS + row) % G;
                 const bool real = row < ck_rows(sq, G, pc.t);

@@ -429,12 +429,14 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  * key: nothing is written for it, its out is 0 and its lse -inf.  Products
  * take 16-bit operands (the softmax weights are rounded to dtype, their sum is
  * not) and accumulate in fp32.  Keys and values of positions below length must
- * be finite; whatever pages hold behind them, NaN included, has no effect.
+ * be finite (a NaN reaches the tokens that see it, a value's perhaps others of
+ * its sequence too); whatever pages hold behind them, NaN included, has no
+ * effect.
  * Positions that are written must lie in pages of one row of the call only.
  * Nothing is allocated, so calls can be captured into graphs; lengths, rows and
  * pages may change between replays, sizes may not.
  *
- * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; N >= 1; pointers
+ * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; 1 <= N <= 2^28; pointers
  * to 16-bit data 16-byte aligned and their strides multiples of 8 elements;
  * P * page_size and total_q * Hq below 2^31 - 4096.  total_q == 0 does nothing.
  */

@@ -263,6 +263,37 @@ def test_bad_numbers_are_reported(what, nq, ln):
         assert (t[0] == v).all() and (t[-1] == v).all()
 
 
+@pytest.mark.parametrize("nq,ln", [([1, 2], [700, 40]), ([200, 70], [1500, 300])], ids=["few", "chunk"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_nan_in_a_key_is_not_lost(nq, ln, dtype):
+    """A NaN in a key that every row sees is in all of their results, wherever in a tile the key lies."""
+    for pos in (0, 1, 9, 17, 33, 63, 65, 66, 127, 129, 400, 537):
+        c = make(nq, ln, 4, 2, 64, 16, dtype=dtype, seed=pos, span=LONG)
+        kp, vp = appended(c)
+        page = int(c["table"][c["row_of"][0], pos // 16])
+        c["kp"][page, pos % 16, 1, 5] = float("nan")
+        out, lse = call(c)
+        assert kda.stream_status() == kda.KDA_OK
+        assert torch.isnan(out[: nq[0], 2:].float()).all() and torch.isnan(lse[: nq[0], 2:]).all()
+        out[: nq[0], 2:], lse[: nq[0], 2:] = 0.0, 0.0
+        o, z, tol, ltol = attention64(c, kp, vp)
+        o[: nq[0], 2:], z[: nq[0], 2:] = 0.0, 0.0
+        assert ((out.double() - o).abs() <= tol).all() and ((lse.double() - z).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("nq", [1, 100], ids=["few", "chunk"])
+def test_sequences_that_overlap_are_reported(nq):
+    """Offsets that go back and name the same tokens again: far more work than total_q allows for, refused or done in bounds."""
+    N = 400
+    c = make([nq] + [0] * (N - 1), [300] * N, 8, 2, 64, 16, seed=1, poison=False, span=LONG)
+    c["cu"].copy_(torch.tensor([0, nq] * (N // 2) + [0], dtype=torch.int32))
+    ob = torch.full((nq + 2, 8, 64), 5.0, dtype=c["q"].dtype, device="cuda")
+    kda.paged_attn(c["q"], c["kp"], c["vp"], c["cu"], c["table"], c["length"], c["scale"], max_q=nq, k_new=c["kn"],
+                   v_new=c["vn"], out=ob[1:-1])
+    assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
+    assert (ob[0] == 5.0).all() and (ob[-1] == 5.0).all()
+
+
 @pytest.mark.parametrize("nq,ln", [([300, 2], [900, 70]), ([1, 1], [9000, 70])], ids=["chunk", "few"])
 def test_waits_that_give_up_are_reported(nq, ln):
     """With no patience at all the chunk kernel's waits run out; the call ends, says so, and the next one works."""
