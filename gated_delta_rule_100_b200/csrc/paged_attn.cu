@@ -24,9 +24,10 @@
 // tile) items, one run per CTA: lengths from 1 to the cache's end load every SM
 // alike.  An item's own cost counts as PA_HEAD units: for 256 sequences of 128 to
 // 16,384 keys, 8 key heads of 128, the call took 653 us with none, 618, 596, 559
-// and 570 us with 1, 2, 4 and 8; 559 us is 6.6 TB/s, the card's copy rate.  A run has at most one item that began before it and one that ends
-// after it; these write their sums to slots, joined by the second kernel in a
-// fixed order (no atomics, so results do not depend on timing).
+// and 570 us with 1, 2, 4 and 8; 559 us is 6.6 TB/s, the card's copy rate.  A run
+// has at most one item that began before it and one that ends after it; these
+// write their sums to slots, joined by the second kernel in a fixed order (no
+// atomics, so results do not depend on timing).
 #include "kda_internal.cuh"
 #include "paged_params.cuh"
 

@@ -11,9 +11,9 @@
 namespace kda {
 
 // One row's partial result over part of its keys: unnormalised sums against a
-// reference m (log2 units, the weights' shift taken off) and l = sum of 2^(x - m).  The first piece of a split
-// item has its rows from part row `head`, the `count` others from `next`,
-// `stride` rows apart.
+// reference m (log2 units, the weights' shift taken off) and l = sum of 2^(x - m).
+// The first piece of a split item has its rows from part row `head`, the `count`
+// others from `next`, `stride` rows apart.
 struct SplitEntry {
     int n, h, t;     // sequence, key head, row tile
     int head, next, count, stride;  // count = 0: nothing to join
@@ -70,11 +70,6 @@ __device__ __forceinline__ int paged_kv_end(const PagedSeq &s, int G, int last_r
     return max(0, s.len - s.nq + r / G + 1);
 }
 
-__device__ __forceinline__ uint16_t f32_to_16(float x, bool bf) {
-    if (bf) return to_bf16_bits(x);
-    const __half h = __float2half_rn(x);
-    return *reinterpret_cast<const uint16_t *>(&h);
-}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
     if constexpr (BF) return pack_bf16x2(lo, hi);
