@@ -26,8 +26,8 @@
 //   value tile: a page holds anything there, and 0 x NaN is NaN.
 //
 // Measured, 2048 new tokens over 65,536 keys, 32 query heads, 8 key heads of 128:
-// 1.74 ms = 1240 TFLOP/s, 74 % of a library product's rate in a burst and 87 %
-// of its sustained one.  A 256 x 128 tile takes about 3240 cycles, of which the
+// 1.67 ms = 1300 TFLOP/s, 77 % of a library product's rate in a burst and 91 %
+// of its sustained one.  A 256 x 128 tile takes about 3100 cycles, of which the
 // tensor cores work 2048: the rest is the way from scores to weights (TMEM load,
 // 2^x, TMEM store and three hand-offs) where a tile's own warps are the only ones
 // that can go on.  Four row tiles would hide it; registers (a row's 64 scores and
@@ -369,6 +369,15 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *r) {
                  "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
+// Waits for the loads; the registers go through it, so that nothing reads them before.
+__device__ __forceinline__ void tm_wait_ld32(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+    asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The products, with descriptors by their low word (address and leading stride);
@@ -430,16 +439,16 @@ struct Poly {
     }
 };
 
-// Weights 2^(x sc - ref) of a row's 64 scores as 16-bit pairs, and their sum
+// Weights 2^(x sc - ref) of a row's N scores as 16-bit pairs, and their sum
 // before the rounding.  MIX: one of eight by the polynomial, which makes up for
 // the exponential unit's rate (512 cycles a warp for 64; so 384 and the FMA
 // pipe's share beside it); it has no 0 for masked keys.
-template <bool BF, bool MIX>
-__device__ __forceinline__ float ck_weights(const uint32_t (&x)[CK_STEP], uint32_t (&y)[CK_STEP / 2], float sc, float ref) {
+template <bool BF, bool MIX, int N>
+__device__ __forceinline__ float ck_weights(const uint32_t (&x)[N], uint32_t *y, float sc, float ref) {
     const Poly<BF> poly(sc, ref);
     float l[4] = {}, nan = 0.f;
 #pragma unroll
-    for (int k = 0; k < CK_STEP; k += 2) {
+    for (int k = 0; k < N; k += 2) {
         const float u = __uint_as_float(x[k]), v = __uint_as_float(x[k + 1]);
         const float a = ex2(fmaf(u, sc, -ref));
         const float b = MIX && k % 8 == 0 ? poly(v) : ex2(fmaf(v, sc, -ref));
@@ -753,29 +762,55 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             bool unset = true;  // some row has no reference yet
             float l = 0.f;
             const float sc = p.scale_log2;
-            for (int j = 0; j < 2 * nt; ++j) {
-                const int h = j & 1;
-                if (h == 0) {
-                    if (!(ok = wait_warp(S::B_S + w, (s_phase + (j >> 1)) & 1))) break;
-                    tc_fence_after();
-                }
-                // both halves' weights lie over the first half's scores, which are read by then
-                const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
+            auto hand_on = [&](int h) {  // the products may begin on this half
+                tm_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive1(S::B_P + w * 2 + h);
+            };
+            for (int i = 0; i < nt; ++i) {
+                if (!(ok = wait_warp(S::B_S + w, (s_phase + i) & 1))) break;
+                tc_fence_after();
+                // Both halves' weights lie over the first half's scores, which are read by then.
                 // Unmasked keys: the weights with the reference there is, looked at afterwards, so that no
                 // maximum stands between scores and weights.  A sum of the 64 up to MOST keeps every weight
-                // there too; past it the step is done again below, from the scores still in TMEM.
-                bool done = false;
-                float sum;
-                if (j < mask_from && !unset) {
-                    uint32_t x[CK_STEP], y[CK_STEP / 2];
-                    tm_ld32(sb, x);
-                    tm_ld32(sb + 32, x + 32);
-                    tmem_wait_ld();
-                    sum = ck_weights<BF, true>(x, y, sc, m * sc - SH);
-                    done = !__any_sync(0xffffffffu, sum > MOST);
-                    if (done) tm_st32(pb, y);
+                // there too; past it the half is done again below, from the scores still in TMEM.  Scores are
+                // loaded 32 ahead (1.67 ms from 1.74), weights handed on at once: with half 0's store left
+                // in flight under the next 32 exponentials 1.75 ms.
+                int from = 0;  // the first half without weights
+                if (2 * i + 1 < mask_from && !unset) {
+                    uint32_t a[32], b[32], y[32], z[32];
+                    const float ref = m * sc - SH;
+                    tm_ld32(ts, a);
+                    tm_wait_ld32(a);
+                    tm_ld32(ts + 32, b);
+                    float sum = ck_weights<BF, true>(a, y, sc, ref);
+                    tm_wait_ld32(b);
+                    tm_ld32(ts + 64, a);
+                    sum += ck_weights<BF, true>(b, y + 16, sc, ref);
+                    if (!__any_sync(0xffffffffu, sum > MOST)) {
+                        tm_st32(ts, y);
+                        l += sum;
+                        from = 1;
+                        hand_on(0);
+                        tm_wait_ld32(a);
+                        tm_ld32(ts + 96, b);
+                        sum = ck_weights<BF, true>(a, z, sc, ref);
+                        
+                        tm_wait_ld32(b);
+                        sum += ck_weights<BF, true>(b, z + 16, sc, ref);
+                        if (!__any_sync(0xffffffffu, sum > MOST)) {
+                            tm_st32(ts + 32, z);
+                            l += sum;
+                            from = 2;
+                            hand_on(1);
+                        }
+                    }
                 }
-                if (!done) {
+#pragma unroll 1
+                for (int h = from; h < 2; ++h) {
+                    const int j = 2 * i + h;
+                    const uint32_t sb = ts + h * CK_STEP, pb = ts + h * (CK_STEP / 2);
                     uint32_t x[CK_STEP], y[CK_STEP / 2];
                     tm_ld32(sb, x);
                     tm_ld32(sb + 32, x + 32);
@@ -795,7 +830,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         l *= f;
                         if (j > 0) {  // the products of earlier tiles are done, those of this one's first half have to be
                             if (h == 1) {
-                                if (!(ok = wait_warp(S::B_HALF + w, (h_phase + (j >> 1)) & 1))) break;
+                                if (!(ok = wait_warp(S::B_HALF + w, (h_phase + i) & 1))) break;
                                 tc_fence_after();
                             }
 #pragma unroll 1
@@ -811,14 +846,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         }
                     }
                     if (unset) unset = __any_sync(0xffffffffu, m == -INFINITY);
-                    sum = ck_weights<BF, false>(x, y, sc, (m == -INFINITY ? 0.f : m * sc) - SH);
+                    l += ck_weights<BF, false>(x, y, sc, (m == -INFINITY ? 0.f : m * sc) - SH);
                     tm_st32(pb, y);
+                    hand_on(h);
                 }
-                l += sum;
-                tm_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive1(S::B_P + w * 2 + h);  // the products may begin on the first half
+                if (!ok) break;
             }
             // the sums, after the last product
             if (ok && (ok = wait_warp(S::B_S + w, (s_phase + nt) & 1))) {
