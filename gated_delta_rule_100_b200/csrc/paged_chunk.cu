@@ -19,15 +19,14 @@
 //   rescaled only when 64 weights add up to more than 2^7 times what the
 //   reference allows (16-bit rounding is relative and the sums are fp32), so
 //   after the first keys hardly ever.
-// - one weight in eight is a polynomial's, which takes work off the exponential
-//   unit.  2048 tokens over 65,536 keys: 1.4 % longer with none, 2.6 % with one in
-//   four.
+// - one weight in sixteen is a polynomial's, which takes work off the exponential
+//   unit.
 // - the rows of masked keys behind the sequence's end are zeroed in the last
 //   value tile: a page holds anything there, and 0 x NaN is NaN.
 //
 // Measured, 2048 new tokens over 65,536 keys, 32 query heads, 8 key heads of 128:
-// 1.67 ms = 1300 TFLOP/s, 77 % of a library product's rate in a burst and 91 %
-// of its sustained one.  A 256 x 128 tile takes about 3100 cycles, of which the
+// 1.62 ms = 1340 TFLOP/s, 80 % of a library product's rate in a burst and 94 %
+// of its sustained one.  A 256 x 128 tile takes about 3000 cycles, of which the
 // tensor cores work 2048: the rest is the way from scores to weights (TMEM load,
 // 2^x, TMEM store and three hand-offs) where a tile's own warps are the only ones
 // that can go on.  Four row tiles would hide it; registers (a row's 64 scores and
@@ -440,9 +439,10 @@ struct Poly {
 };
 
 // Weights 2^(x sc - ref) of a row's N scores as 16-bit pairs, and their sum
-// before the rounding.  MIX: one of eight by the polynomial, which makes up for
-// the exponential unit's rate (512 cycles a warp for 64; so 384 and the FMA
-// pipe's share beside it); it has no 0 for masked keys.
+// before the rounding.  MIX: one of sixteen by the polynomial, which takes work
+// off the exponential unit (512 cycles a warp for 64); it has no 0 for masked keys.
+// 2048 tokens over 65,536 keys: 1.68 ms with none, 1.635 with one in 32, 1.62 with
+// one in 16, 1.625 with one in 8, 1.68 with three in 16 and one in 4.
 template <bool BF, bool MIX, int N>
 __device__ __forceinline__ float ck_weights(const uint32_t (&x)[N], uint32_t *y, float sc, float ref) {
     const Poly<BF> poly(sc, ref);
@@ -451,10 +451,10 @@ __device__ __forceinline__ float ck_weights(const uint32_t (&x)[N], uint32_t *y,
     for (int k = 0; k < N; k += 2) {
         const float u = __uint_as_float(x[k]), v = __uint_as_float(x[k + 1]);
         const float a = ex2(fmaf(u, sc, -ref));
-        const float b = MIX && k % 8 == 0 ? poly(v) : ex2(fmaf(v, sc, -ref));
+        const float b = MIX && k % 16 == 0 ? poly(v) : ex2(fmaf(v, sc, -ref));
         l[k & 2] += a;
         l[(k & 2) + 1] += b;
-        if (MIX && k % 8 == 0) asm("max.NaN.f32 %0, %0, %1;" : "+f"(nan) : "f"(v));  // which the polynomial's clamp drops
+        if (MIX && k % 16 == 0) asm("max.NaN.f32 %0, %0, %1;" : "+f"(nan) : "f"(v));  // which the polynomial's clamp drops
         y[k / 2] = pack16x2<BF>(a, b);
     }
     const float sum = (l[0] + l[1]) + (l[2] + l[3]);
@@ -775,8 +775,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // Unmasked keys: the weights with the reference there is, looked at afterwards, so that no
                 // maximum stands between scores and weights.  A sum of the 64 up to MOST keeps every weight
                 // there too; past it the half is done again below, from the scores still in TMEM.  Scores are
-                // loaded 32 ahead (1.67 ms from 1.74), weights handed on at once: with half 0's store left
-                // in flight under the next 32 exponentials 1.75 ms.
+                // loaded 32 ahead (1.67 ms from 1.74) and weights handed on at once (1.75 ms with half 0's
+                // store left in flight under the next 32 exponentials).
                 int from = 0;  // the first half without weights
                 if (2 * i + 1 < mask_from && !unset) {
                     uint32_t a[32], b[32], y[32], z[32];
@@ -799,8 +799,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         
                         tm_wait_ld32(b);
                         sum += ck_weights<BF, true>(b, z + 16, sc, ref);
+                        tm_st32(ts + 32, z);  // over scores of the half before: before the look at the sum, 1.5 % off
                         if (!__any_sync(0xffffffffu, sum > MOST)) {
-                            tm_st32(ts + 32, z);
                             l += sum;
                             from = 2;
                             hand_on(1);
