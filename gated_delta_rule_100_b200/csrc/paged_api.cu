@@ -44,7 +44,7 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
         return KDA_ERR_INVALID_ARG;
     if (total_q > 0 && max_q < 1) return KDA_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
-    if (N > (1 << 28) || (long long)P * page_size > 0x7ffff000LL || (long long)total_q * Hq > 0x7ffff000LL)
+    if (N > (1 << 22) || (long long)P * page_size > 0x7ffff000LL || (long long)total_q * Hq > 0x7ffff000LL)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

@@ -497,8 +497,10 @@ static cudaError_t launch_join_t(const PagedParams &p, const int *count, int max
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int groups = tile_rows > 64 ? 8 : 2;  // blocks of eight warps over an item's rows
-    cfg.gridDim = dim3(max_entries < 2 * sms ? max_entries : 2 * sms, groups);
+    // blocks of eight warps over an item's rows: of 256 rows a warp takes two, one after the other (four, with
+    // half the blocks and twice the entries at once: 0.6 us more)
+    const int groups = tile_rows > 64 ? 16 : 2, entries = tile_rows > 64 ? sms : 2 * sms;
+    cfg.gridDim = dim3(max_entries < entries ? max_entries : entries, groups);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = at;

@@ -104,8 +104,10 @@ constexpr int CK_CAND = 16;
 __device__ __constant__ int ck_div[CK_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64, 128, 256};
 
 __device__ void ck_plan(const ChunkParams &c, int d) {
-    __shared__ unsigned long long s_w, s_wa, s_q, s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND];  // of one key head; rows in eights
-    __shared__ unsigned s_a;
+    // of one key head; rows in eights.  32 bits hold them: there are below 2^24 tiles, and rows of
+    // candidates with more pieces than there is room for do not count
+    __shared__ unsigned s_pieces[2 * CK_CAND], s_rows8[2 * CK_CAND], s_a;
+    __shared__ unsigned long long s_w, s_wa, s_q;
     __shared__ int s_max, s_ma, s_items, s_step, s_phi, s_entries, s_part, s_sum[33];
     const PagedParams &p = c.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5, G = p.G;
@@ -149,11 +151,12 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     const float phi1 = (float)(all / c.sms * c.sms) / fmaxf((float)all, 1.f);
     // whole tiles of a sequence: ranks below, counted from the one with the most keys
     auto whole = [&](int tiles, int phi) { return phi ? (int)(tiles * phi1) : 0; };
-    {   // a lane a candidate; few sequences share the warps among their tiles
-        const int q = lane / CK_CAND, split = max(1, warps / p.N);
+    const int split = max(1, warps / p.N);  // few sequences share the warps: here among their tiles, below among the heads
+    {   // a lane a candidate
+        const int q = lane / CK_CAND;
         const int step = (s_max + ck_div[lane % CK_CAND] - 1) / ck_div[lane % CK_CAND];
-        unsigned long long pieces = 0, rows8 = 0, wa = 0;
-        unsigned na = 0;
+        unsigned long long wa = 0;
+        unsigned na = 0, pieces = 0, rows8 = 0;
         int ma = 0;
         for (int v = warp; v < p.N * split; v += warps) {
             const PagedSeq s = paged_seq(p, v % p.N, false);
@@ -180,14 +183,15 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
     if (warp == 0) {
         const int q = lane / CK_CAND, j = lane % CK_CAND, step = (s_max + ck_div[j] - 1) / ck_div[j];
         const float S = (float)c.sms, R = (float)s_rows8[lane] * 8.f * p.Hkv;
-        const float pa = q ? (float)s_a * p.Hkv : 0.f, ta = q && s_a ? (float)s_wa / s_a + 3.f : 0.f;
-        const float pb = (float)s_pieces[lane] * p.Hkv, tb = pb > 0.f ? (float)(s_w - (q ? s_wa : 0)) * p.Hkv / pb + 3.f : 3.f;
-        const float ka = ceilf(pa / S), early = (ka * S - pa) * floorf(ta / tb);
-        float cost = ka * ta + (pb > early ? ceilf((pb - early) / S) * tb : 0.f);
+        const float pa = q ? (float)s_a * p.Hkv : 0.f, ta = q && s_a ? __fdividef((float)s_wa, (float)s_a) + 3.f : 0.f;
+        const float pb = (float)s_pieces[lane] * p.Hkv,
+                    tb = pb > 0.f ? __fdividef((float)(s_w - (q ? s_wa : 0)) * p.Hkv, pb) + 3.f : 3.f;
+        const float ka = ceilf(__fdividef(pa, S)), early = (ka * S - pa) * floorf(__fdividef(ta, tb));
+        float cost = ka * ta + (pb > early ? ceilf(__fdividef(pb - early, S)) * tb : 0.f);
         cost = fmaxf(cost, max(pa > 0.f ? s_ma : 0, pb > 0.f ? step : 0) + 3.f);  // no less than the longest
         if (R > 0.f) cost += 3.f + R * d * 8.f * 1.2e-7f;
         // what the workspace has no room for is out (not the uncut items, which it always has room for)
-        const unsigned long long np = (s_pieces[lane] + (q ? s_a : 0u)) * p.Hkv, nr = s_rows8[lane] * 8ull * p.Hkv;
+        const unsigned long long np = (unsigned long long)(s_pieces[lane] + (q ? s_a : 0u)) * p.Hkv, nr = s_rows8[lane] * 8ull * p.Hkv;
         if (lane > 0 && (np > (unsigned long long)c.max_pieces || nr > (unsigned long long)c.max_rows)) cost = 3.0e38f;
         float best = cost;
 #pragma unroll
@@ -241,45 +245,50 @@ __device__ void ck_plan(const ChunkParams &c, int d) {
         at += k;
     }
     __syncthreads();
-    for (int n = warp; n < p.N; n += warps) {
+    for (int v = warp; v < p.N * split; v += warps) {
+        const int n = v % p.N, h0 = v / p.N, heads = (p.Hkv - h0 + split - 1) / split;  // key heads h0, h0 + split, ..
         const PagedSeq s = paged_seq(p, n, false);
         const int tiles = ck_tiles(s, G), a = whole(tiles, phi);
-        const int f0 = c.base[n + p.N], r0 = c.base[n + 2 * p.N];
+        const int w0 = c.base[n], f0 = c.base[n + p.N], r0 = c.base[n + 2 * p.N];
         const int full_head = (c.base[n + p.N + 1] - f0) / p.Hkv;
         const int rest_head = ((n + 1 < p.N ? c.base[n + 2 * p.N + 1] : total) - r0) / p.Hkv;
         int full_before = 0, rest_before = 0;
-        for (int t0 = 0; t0 < tiles; t0 += 32) {
-            const int rank = t0 + lane, t = tiles - 1 - rank;  // the longest first
-            const bool w1 = rank < a;
-            const int k = t >= 0 ? ck_keys(s, G, t) : 0, big = 2 * (k % step) >= step,
-                      full = w1 ? 0 : k / step + big, rest = !w1 && !big && k % step != 0;
+        for (int t0 = 0; t0 < tiles && heads > 0; t0 += 32) {
+            const int tl = tiles - 1 - t0 - lane;  // a lane a tile, the longest first
+            const bool wl = t0 + lane < a;
+            const int kl = tl >= 0 ? ck_keys(s, G, tl) : 0, big = 2 * (kl % step) >= step,
+                      full = wl ? 0 : kl / step + big, rest = !wl && !big && kl % step != 0;
             int fi = full, ri = rest;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int uf = __shfl_up_sync(0xffffffffu, fi, o), ur = __shfl_up_sync(0xffffffffu, ri, o);
                 if (lane >= o) { fi += uf; ri += ur; }
             }
-            if (t >= 0) {
-                const int r = ck_rows(s, G, t), ns = w1 ? 1 : full + rest;
-                for (int h = 0; h < p.Hkv; ++h) {
-                    int part = -1;
-                    if (ns > 1) {
-                        part = atomicAdd(&s_part, ns * r);
-                        const int e = atomicAdd(&s_entries, 1);
-                        if (e < c.max_entries && part + ns * r <= c.max_rows)
-                            p.entries[e] = {n, h, t, part, part + r, ns - 1, r};
-                        else report(p.st, DEV_BAD_ARG);  // only where cu_q or length change meanwhile
-                    }
-                    for (int j = 0; j < ns; ++j) {
-                        const long long i = w1 ? (long long)c.base[n] + (long long)h * a + rank
-                                          : j < full ? f0 + (long long)h * full_head + full_before + fi - full + j
-                                                     : r0 + (long long)h * rest_head + rest_before + ri - 1;
-                        if ((unsigned long long)i >= (unsigned long long)c.max_pieces) { report(p.st, DEV_BAD_ARG); continue; }
-                        const int kv0 = j * step, row = part < 0 ? -1 : part + j * r;
-                        // a piece without room for its sums is left empty
-                        const bool room = part < 0 || part + ns * r <= c.max_rows;
-                        c.pieces[i] = {n, h, t, kv0, !room ? kv0 : w1 ? k : min(k, kv0 + step), row, s, {0, 0}};
-                    }
+            const int work = min(32, tiles - t0) * heads;
+            for (int b = 0; b < work; b += 32) {  // then a lane an item: a tile of a head
+                const int of = min((b + lane) / heads, 31), h = h0 + (b + lane) % heads * split;
+                const int k = __shfl_sync(0xffffffffu, kl, of), nf = __shfl_sync(0xffffffffu, full, of),
+                          nr = __shfl_sync(0xffffffffu, rest, of), fb = full_before + __shfl_sync(0xffffffffu, fi, of) - nf,
+                          rb = rest_before + __shfl_sync(0xffffffffu, ri, of) - 1;
+                if (b + lane >= work) continue;
+                const int rank = t0 + of, t = tiles - 1 - rank;
+                const bool w1 = rank < a;
+                const int r = ck_rows(s, G, t), ns = w1 ? 1 : nf + nr;
+                int part = -1;
+                if (ns > 1) {
+                    part = atomicAdd(&s_part, ns * r);
+                    const int e = atomicAdd(&s_entries, 1);
+                    if (e < c.max_entries && part + ns * r <= c.max_rows)
+                        p.entries[e] = {n, h, t, part, part + r, ns - 1, r};
+                    else report(p.st, DEV_BAD_ARG);  // only where cu_q or length change meanwhile
+                }
+                // a piece without room for its sums is left empty
+                const bool room = part < 0 || part + ns * r <= c.max_rows;
+                for (int j = 0; j < ns; ++j) {
+                    const unsigned i = w1 ? w0 + h * a + rank : j < nf ? f0 + h * full_head + fb + j : r0 + h * rest_head + rb;
+                    if (i >= (unsigned)c.max_pieces) { report(p.st, DEV_BAD_ARG); continue; }
+                    const int kv0 = j * step;
+                    c.pieces[i] = {n, h, t, kv0, !room ? kv0 : w1 ? k : min(k, kv0 + step), part < 0 ? -1 : part + j * r, s, {0, 0}};
                 }
             }
             full_before += __shfl_sync(0xffffffffu, fi, 31);

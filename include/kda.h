@@ -436,7 +436,7 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  * Nothing is allocated, so calls can be captured into graphs; lengths, rows and
  * pages may change between replays, sizes may not.
  *
- * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; 1 <= N <= 2^28; pointers
+ * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; 1 <= N <= 2^22; pointers
  * to 16-bit data 16-byte aligned and their strides multiples of 8 elements;
  * P * page_size and total_q * Hq below 2^31 - 4096.  total_q == 0 does nothing.
  */
