@@ -805,7 +805,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         tm_wait_ld32(a);
                         tm_ld32(ts + 96, b);
                         sum = ck_weights<BF, true>(a, z, sc, ref);
-                        
                         tm_wait_ld32(b);
                         sum += ck_weights<BF, true>(b, z + 16, sc, ref);
                         tm_st32(ts + 32, z);  // over scores of the half before: before the look at the sum, 1.5 % off
@@ -814,6 +813,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             from = 2;
                             hand_on(1);
                         }
+                    } else {
+                        tm_wait_ld32(a);  // nothing may land in registers that are others' by then
                     }
                 }
 #pragma unroll 1
