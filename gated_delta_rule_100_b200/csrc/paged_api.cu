@@ -52,11 +52,13 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
 // The kernel of few rows runs up to kFewRows rows of a sequence and key head (new tokens times
 // query heads), and where there are at most kFewUnits 64-key units a CTA, as many as the sizes
 // allow; the chunk kernel otherwise.  Few rows are bound by memory and want many CTAs' loads; the
-// chunk kernel's tiles are 128 rows whatever there is, and its plan, pieces and join take some 15 us.
+// chunk kernel's tiles are 128 rows whatever there is, and its plan, pieces and join take some 12 us.
 // Measured (few rows / chunk kernel, us), 4 key heads of 128, 64 sequences of 128 to 8192 keys: 24
-// rows 83 / 90, 32 rows 81 / 93, 64 rows 143 / 99; of 64: 32 rows 52 / 82.  By units a CTA: 5 (256
-// tokens over 1024, 8 heads of 64) 20 / 35, 8 (100 over 3000, 2 of 128) 26 / 40, 9 and 10: 37 / 32
-// and 23 / 24, 17 (16 chunks of 16 over 500) 30 / 27, 28 (512 over 512, 8 of 128) 50 / 30.
+// rows 81 / 84, 32 rows 83 / 83, 40 rows 132 / 95, 64 rows 143 / 89; of 64: 32 rows 51 / 72, 64 rows
+// 88 / 77.  By units a CTA: 5 (256 tokens over 1024, 8 heads of 64) 21 / 24, 5 (64 over 4000, 4 of 64
+// with 2 queries) 17 / 26, 6 (300 over 1500, 4 of 128) 31 / 31, 7 (512 over 512, 8 of 128) 30 / 28, 8
+// (100 over 3000, 2 of 128 with 4) 26 / 33, 9 (16 chunks of 16 over 500) 17 / 25, 11 (200 over 2000, 2
+// of 128 with 4) 33 / 31.
 constexpr int kFewRows = 32, kFewUnits = 9;
 
 // Keys of a full table up to which the kernel of few rows takes items whole: one launch, no join
