@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
             const int row = done.t * PA_ROWS + r;
             if (begins && ends) {
                 if (row < done.s.nq * G) {
-                    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
                     const long long tok = done.s.q0 + row / G;
                     const int head = done.h * G + row % G;
                     uint2 y;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                     y.y = pack16x2<BF>(a.z * inv, a.w * inv);
                     *reinterpret_cast<uint2 *>(p.out + (tok * p.Hq + head) * D + col) = y;
                     if (p.lse != nullptr && col == 0)
-                        p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
+                        p.lse[tok * p.Hq + head] = row_lse(M, L);
                 }
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + ((long long)slot * PA_ROWS + r) * D + col) = a;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
                     }
                 }
             }
-            const float inv = M == -INFINITY ? 0.f : 1.f / L;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
             const int row = e.t * tile_rows + r, head = e.h * p.G + row % p.G;
             const long long tok = s.q0 + row / p.G;
 #pragma unroll
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
                 *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + head) * D + lane * V + j) =
                     pack16x2<BF>(a[j] * inv, a[j + 1] * inv);
             if (p.lse != nullptr && lane == 0)
-                p.lse[tok * p.Hq + head] = M == -INFINITY ? -INFINITY : M * LN2 + logf(L);
+                p.lse[tok * p.Hq + head] = row_lse(M, L);
         }
     }
 }

@@ -898,7 +898,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (real) {
                     if (!whole) p.part_ml[pc.part_row + row] = make_float2(m == -INFINITY ? m : m * sc - SH, l);
                     else if (p.lse != nullptr)
-                        p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = m == -INFINITY ? -INFINITY : (m * sc - SH) * LN2 + logf(l);
+                        p.lse[(long long)(sq.q0 + tok) * p.Hq + head] = row_lse(m * sc - SH, l);
                 }
                 tc_fence_before();
             }

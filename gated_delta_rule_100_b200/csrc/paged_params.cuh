@@ -95,4 +95,9 @@ __host__ __device__ constexpr float weight_shift() { return BF ? 0.f : 8.f; }
 
 constexpr float LN2 = 0.69314718055994531f;
 
+// lse of a row from its reference m (log2 units) and sum l.  What tells a row without keys is
+// l == 0: a row whose every score is NaN has m = -inf as well (maxima pass NaN over), and l = NaN,
+// which is its lse.
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : m * LN2 + logf(l); }
+
 }  // namespace kda
