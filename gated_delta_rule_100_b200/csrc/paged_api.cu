@@ -134,7 +134,8 @@ kda::PagesParams pages_params(int *table, int *length, int *ref, int R, int P, i
 }
 int pool_check(const void *pool, long long outer, long long outer_stride, long long page_stride, long long page_bytes,
                int num_pages) {
-    if (pool == nullptr || outer < 0 || page_bytes < 1 || num_pages < 1 || outer_stride < 0 || page_stride < 0)
+    // a pool of no layers has no memory
+    if ((pool == nullptr && outer != 0) || outer < 0 || page_bytes < 1 || num_pages < 1 || outer_stride < 0 || page_stride < 0)
         return KDA_ERR_INVALID_ARG;
     // pages that overlap would be read and written at once
     if ((num_pages > 1 && page_stride < page_bytes) || (outer > 1 && outer_stride < page_bytes)) return KDA_ERR_INVALID_ARG;
