@@ -674,7 +674,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     if (cp < vcopies) tma_load_4d(base + S::OFF_V + st * S::TILE + put, &tm_v, bar(bi), kb * 64, vtok, pc.h, vpage);
                     if (cp < copies) tma_load_4d(base + S::OFF_K + (st ^ 1) * S::TILE + put, &tm_k, bar(bi), kb * 64, tok0, pc.h, page);
                     if (tail) {
-                        ok = wait_warp(S::B_TAIL, tails & 1);
+                        if (!(ok = wait_warp(S::B_TAIL, tails & 1))) {
+                            // the values are on their way still: nothing is zeroed or handed on, and this
+                            // memory stays the CTA's until they are here
+                            if (lane == 0) mbar_wait(bar(S::B_TAIL), tails & 1, ~0ull, p.st);
+                            __syncwarp();
+                            break;
+                        }
                         ++tails;
                         for (int k = lane; k < (CK_KT - vvalid) * (D / 64) * 8; k += 32) {
                             const int row = vvalid + k / (D / 64 * 8), b = k / 8 % (D / 64), ch = k % 8;
@@ -693,8 +699,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     else if ((tok0 += CK_KT) == p.page_size) { tok0 = 0; ++pi; }
                 }
             }
-            if (!ok && lane == 0)  // leave no copy in flight into this CTA's memory
+            // Leave no copy in flight into this CTA's memory.  This warp may have loaded all there is when another
+            // one gives up, so it looks whether it has itself or not.
+            if (lane == 0)
                 for (uint32_t b = g >= 2 ? g - 2 : 0; b < g; ++b) mbar_wait(bar(S::B_FULL + (b & 1)), (b >> 1) & 1, ~0ull, p.st);
+            __syncwarp();
         } else if (warp == CK_MMA) {
             // ------------------------------------------------ issuer (one lane issues)
             Issuer<D, BF> is = {base, tmem, tries};
@@ -714,10 +723,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 s_abort = 1;
                 if (lane == 0) report(p.st, DEV_TIMEOUT);
             }
-            if (lane == 0 && s_abort) {  // leave no product in flight
+            // Leave no product in flight: the rows that wait for the last ones may give up after this warp is
+            // done.  A commit tracks the products of the thread that it is made by, which is the one elected.
+            if (elect_lane()) {
                 umma_commit(bar(S::B_DRAIN));
                 mbar_wait(bar(S::B_DRAIN), 0, ~0ull, p.st);
             }
+            __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CK_REGS_ROWS));
@@ -905,6 +917,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             s_phase += nt + 1;
             h_phase += nt;
         }
+        __syncwarp();
+        tm_wait_st();  // weights that are done again, where the wait before that gave up
     }
     __syncwarp();
     tc_fence_before();

@@ -46,3 +46,32 @@ def test_a_row_of_nan_scores_is_no_empty_row(nq, ln, span, dtype):
     assert kda.stream_status() == kda.KDA_OK
     assert torch.isnan(out[hit].float()).all() and torch.isnan(lse[hit]).all()
     near(c, out, lse, want, hit)
+
+
+@pytest.mark.parametrize("nq,ln,d", [([300, 2], [900, 70], 128), ([40], [5001], 64), ([129] * 9, [1000 + 37 * i for i in range(9)], 128)])
+def test_calls_that_give_up_anywhere_end_in_order(nq, ln, d):
+    """Waits cut to a few tries run out at different places: before the first product, at a tail's values, at the last
+    products.  Every call ends, says so or is right, leaves the memory beside its buffers alone, and the next is right."""
+    c = make(nq, ln, 8, 2, d, 64, seed=12, span=LONG, q_scale=4.0)
+    kp, vp = appended(c)
+    want = attention64(c, kp, vp)
+    ob = torch.full((c["total"] + 2, 8, d), 5.0, dtype=c["q"].dtype, device="cuda")
+    gave_up = 0
+    for tries in (1, 1, 2, 2, 3, 4, 5, 6, 8, 12):
+        try:
+            kda.set_wait_limit(tries)
+            lse = call(c, out=ob[1:-1])[1]
+            status = kda.stream_status()
+        finally:
+            kda.set_wait_limit(0)
+        assert status in (kda.KDA_OK, kda.KDA_ERR_TIMEOUT)
+        gave_up += status != kda.KDA_OK
+        if status == kda.KDA_OK:
+            near(c, ob[1:-1], lse, want)
+        assert (ob[0] == 5.0).all() and (ob[-1] == 5.0).all()
+        out, lse = call(c)
+        assert kda.stream_status() == kda.KDA_OK
+        near(c, out, lse, want)
+        for x, y in ((c["kp"], kp), (c["vp"], vp)):
+            assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+    assert gave_up
