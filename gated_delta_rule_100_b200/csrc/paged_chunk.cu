@@ -81,7 +81,7 @@ struct CkShape {
     // read [stage], a tail's copies, the end of all products, pieces handed on [2], taken [2]
     static constexpr int B_Q = 0, B_S = 2, B_P = 4, B_HALF = 8, B_FULL = 10, B_EMPTY = 12, B_TAIL = 14, B_DRAIN = 15, B_WORK = 16,
                          B_FREE = 18, NBAR = 20;
-    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;          // and four words
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 32;          // and five words
     static constexpr uint32_t TM_S = 0, TM_O = 256;               // columns: S0, S1, O0, O1
 };
 
@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(512) paged_plan_kernel(const ChunkParams c) {
 // A bounded wait of at most `tries` tries, in five instructions.  mbar_wait reads
 // %globaltimer after its first miss, which takes longer than most waits here (it
 // cost each contended wait 300 to 600 cycles), and is long where the
-// instruction cache is short of room.
+// instruction cache is short of room.  A try that misses sleeps for 4 us (measured, with
+// one warp waiting and with twelve), so CK_TRIES of them are the second that a bounded
+// wait lasts elsewhere.
+constexpr uint32_t CK_TRIES = 1u << 18;
 __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
     uint32_t ok;
     asm volatile(
@@ -570,14 +573,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     volatile int *words = reinterpret_cast<volatile int *>(sm + S::OFF_BAR + S::NBAR * 8);
     volatile int *s_piece = words;       // [2] the pieces handed on
     volatile int &s_abort = words[2];
+    volatile int &s_loaded = words[4];   // pairs of tiles loaded so far
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.G;
-    const uint32_t tries = p.st.wait_polls < (1u << 20) ? (uint32_t)p.st.wait_polls : 1u << 20;  // of some 50 ns up
+    const uint32_t tries = p.st.wait_polls < CK_TRIES ? (uint32_t)p.st.wait_polls : CK_TRIES;
     auto bar = [&](int i) { return base + S::OFF_BAR + i * 8; };
 
     if (tid == 0) {
         for (int i = 0; i < S::NBAR; ++i)
             mbar_init(bar(i), (i < S::B_S || (i >= S::B_P && i < S::B_P + 4)) ? 4u : (i == S::B_FREE || i == S::B_FREE + 1) ? CK_RW + 1u : 1u);
-        s_abort = 0;
+        s_abort = s_loaded = 0;
         fence_mbar_init();
     }
     if (warp == CK_MMA) {
@@ -610,8 +614,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     // The loader claims pieces and hands each on through two slots, so that it can run ahead:
     // it loads the next piece's keys while the rows of this one are being finished.
     // take(): the k-th piece (-1: no more); a warp is done with its slot once it has read it.
+    // A tile without rows of its own waits here while the other one works on a piece, which may
+    // take longer than a wait may: this one goes on for as long as something is loaded meanwhile.
     auto take = [&](uint32_t k) -> int {
-        if (!wait_warp(S::B_WORK + (k & 1), (k >> 1) & 1)) return -1;
+        if (!__all_sync(0xffffffffu, ck_wait(bar(S::B_WORK + (k & 1)), (k >> 1) & 1, tries))) {
+            int seen, now = 0;
+            do {
+                seen = now;
+                now = s_loaded;
+                if (!__any_sync(0xffffffffu, now != seen)) {
+                    s_abort = 1;
+                    report(p.st, DEV_TIMEOUT);
+                    return -1;
+                }
+            } while (!__all_sync(0xffffffffu, ck_wait(bar(S::B_WORK + (k & 1)), (k >> 1) & 1, tries)));
+        }
         const int at = s_piece[k & 1];
         __syncwarp();
         if (lane == 0) arrive1(S::B_FREE + (k & 1));
@@ -691,6 +708,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         __syncwarp();
                         if (lane == 0) arrive1(S::B_FULL + st);
                     }
+                    if (lane == 0) s_loaded = (int)g + 1;
                     vpage = page;
                     vtok = tok0;
                     vcopies = copies;

@@ -75,3 +75,22 @@ def test_calls_that_give_up_anywhere_end_in_order(nq, ln, d):
         for x, y in ((c["kp"], kp), (c["vp"], vp)):
             assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
     assert gave_up
+
+
+def test_a_tile_without_rows_outlasts_a_long_piece():
+    """40 rows an item leave half of a CTA's rows idle for as long as its piece takes: that wait ends by what is being
+    loaded, not by the limit of a step's waits.  As many items as SMs, so that no item is cut: 1500 steps of keys each,
+    at a limit of about 64 x 4 us."""
+    N = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    c = make([10], [200_000], 8, 2, 64, 64, seed=13, poison=False)
+    kp, vp = appended(c)
+    o, z, tol, ltol = attention64(c, kp, vp)
+    lse = torch.zeros((10 * N, 8), device="cuda")
+    try:
+        kda.set_wait_limit(64)
+        out = kda.paged_attn(c["q"].repeat(N, 1, 1), kp, vp, torch.arange(0, 10 * N + 1, 10, device="cuda", dtype=torch.int32),
+                             c["table"].repeat(N, 1), c["length"].repeat(N), c["scale"], max_q=10, lse=lse)
+        assert kda.stream_status() == kda.KDA_OK
+    finally:
+        kda.set_wait_limit(0)
+    assert ((out.view(N, 10, 8, 64).double() - o).abs() <= tol).all() and ((lse.view(N, 10, 8).double() - z).abs() <= ltol).all()
