@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/kda.h"
 #include "kda_internal.cuh"
 #include "paged_params.cuh"
@@ -36,6 +38,23 @@ int device() {
     return cudaGetDevice(&dev) == cudaSuccess ? dev : 0;
 }
 int to_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+// Whether cells of `width`, extent[i] of them stride[i] apart along axis i, lie clear of one
+// another: along the axes by stride, each step leads past all that the axes before it reach.
+// (Layouts that mesh without that, such as steps of 2 and 3 cells, count as overlapping.)
+template <int N>
+bool apart(const long long (&stride)[N], const long long (&extent)[N], long long width) {
+    int order[N];
+    for (int i = 0; i < N; ++i) order[i] = i;
+    std::sort(order, order + N, [&](int a, int b) { return stride[a] < stride[b]; });
+    __int128 reach = width;
+    for (const int i : order) {
+        if (extent[i] < 2) continue;
+        if (stride[i] < reach) return false;
+        reach += (__int128)(extent[i] - 1) * stride[i];
+    }
+    return true;
+}
 
 // ------------------------------------------------------------- attention ----
 // Sizes that paged attention takes at all (0: yes).
@@ -201,13 +220,16 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
     const long long *ps = page_strides ? page_strides : dense;
     if (q_stride < (long long)Hq * d || (k_new && (k_stride < row || v_stride < row))) return KDA_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i) {
-        if (ps[i] < d || ps[i] > (1LL << 38)) return KDA_ERR_INVALID_ARG;  // tokens, heads and pages do not overlap
+        if (ps[i] < d || ps[i] > (1LL << 38)) return KDA_ERR_INVALID_ARG;
         if (ps[i] % 8) return KDA_ERR_ALIGNMENT;
     }
     if (q_stride % 8 || (k_new && (k_stride % 8 || v_stride % 8)) || !al(q, 16) || !al(k_new, 16) || !al(v_new, 16) ||
         !al(k_pages, 16) || !al(v_pages, 16) || !al(out, 16) || !al(lse, 4) || !al(cu_q, 4) || !al(page_table, 4) ||
         !al(length, 4) || !al(rows, 4) || !al(workspace, 16))
         return KDA_ERR_ALIGNMENT;
+    // the new tokens would be written over one another
+    const long long places[3] = {num_pages, page_size, Hkv};
+    if (k_new && !(apart({ps[0], ps[1], ps[2]}, places, d) && apart({ps[3], ps[4], ps[5]}, places, d))) return KDA_ERR_INVALID_ARG;
     if (total_q == 0) return KDA_OK;
     const AttnPlan pl = attn_plan(N, total_q, max_q, Hq, Hkv, d, page_size, P);
     if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return KDA_ERR_INVALID_ARG;

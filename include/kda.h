@@ -417,7 +417,10 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  *   q_stride, k_stride, v_stride : elements between tokens of q, k_new, v_new
  *                (heads and channels are dense)
  *   page_strides : HOST array of 6, elements between pages, tokens and heads of
- *                k_pages, then of v_pages; NULL for the dense layout above
+ *                k_pages, then of v_pages; NULL for the dense layout above.  Where
+ *                the call writes, places do not overlap (along the axes by
+ *                stride, each step leads past all that the ones before reach),
+ *                and keys and values share none
  *   dtype      : KDA_BF16 or KDA_FP16, of q, k, v and out
  *   workspace  : kda_paged_attn_workspace_bytes() bytes, 16-byte aligned, of
  *                the caller (NULL when that is 0); a call's alone until it is

@@ -94,3 +94,16 @@ def test_a_tile_without_rows_outlasts_a_long_piece():
     finally:
         kda.set_wait_limit(0)
     assert ((out.view(N, 10, 8, 64).double() - o).abs() <= tol).all() and ((lse.view(N, 10, 8).double() - z).abs() <= ltol).all()
+
+
+def test_the_binding_refuses_places_that_overlap():
+    c = make([1, 3], [40, 20], 4, 2, 64, 16, seed=3, poison=False)
+    shape, good = c["kp"].shape, c["kp"]
+    flat = torch.zeros(shape[0] * 16 * 2 * 64 + 64, dtype=torch.bfloat16, device="cuda")
+    for strides in ((2048, 64, 64, 1), (1024, 128, 64, 1), (2048, 128, 128, 1)):
+        for name in ("kp", "vp"):
+            with pytest.raises(kda.KdaError):
+                call({**c, name: flat.as_strided(shape, strides)})
+    assert (flat == 0).all()
+    out, lse = call({**c, "kp": good.clone()})
+    near(c, out, lse, attention64(c, *appended(c)))
