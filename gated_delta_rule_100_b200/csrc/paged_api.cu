@@ -157,7 +157,8 @@ int pool_check(const void *pool, long long outer, long long outer_stride, long l
     if ((pool == nullptr && outer != 0) || outer < 0 || page_bytes < 1 || num_pages < 1 || outer_stride < 0 || page_stride < 0)
         return KDA_ERR_INVALID_ARG;
     // pages that overlap would be read and written at once
-    if ((num_pages > 1 && page_stride < page_bytes) || (outer > 1 && outer_stride < page_bytes)) return KDA_ERR_INVALID_ARG;
+    const long long extent[2] = {num_pages, outer};
+    if (!apart({page_stride, outer_stride}, extent, page_bytes)) return KDA_ERR_INVALID_ARG;
     if (!al(pool, 16) || page_bytes % 16 || page_stride % 16 || outer_stride % 16) return KDA_ERR_ALIGNMENT;
     if (outer > (1 << 24)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;

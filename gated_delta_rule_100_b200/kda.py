@@ -683,7 +683,8 @@ def _pool(t, num_pages, dev):
     page = want * es
     ps = st[1] * es if num_pages > 1 else page
     p, outer, os = t.data_ptr(), shape[0], st[0] * es if shape[0] > 1 else ps * num_pages
-    if (p | os | ps | page) & 15 or page < 1 or ps < page or os < page or outer > 1 << 24:
+    apart = ps >= page and (os >= ps * num_pages or ps >= os * outer and os >= page)
+    if (p | os | ps | page) & 15 or page < 1 or not apart or outer > 1 << 24:
         # refused here, before a call that changes the table has run
         rc = load().kda_pages_copy(p, outer, os, ps, page, num_pages, None, None, 0, None)
         if rc != KDA_OK:

@@ -519,7 +519,8 @@ KDA_API int kda_pages_compact_pool(void *pool, long long outer, long long outer_
  * src, dst: int32 [n].  A pair -1, -1 is skipped.  A destination must not be
  * named a second time, as a destination or as a source: such a pair is left
  * out and reported.  pool, page_bytes and the strides (in bytes): multiples of
- * 16; pages do not overlap.
+ * 16; pages do not overlap (those of one o lie inside the step to the next, or
+ * those of one number inside the step to the next number).
  */
 KDA_API int kda_pages_copy(void *pool, long long outer, long long outer_stride, long long page_stride,
                   long long page_bytes, int num_pages, const int *src, const int *dst, int n, void *stream);

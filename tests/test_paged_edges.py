@@ -64,3 +64,18 @@ def test_strides_along_one_place_say_nothing(lib):
     assert attn(lib, (64, 64, 64) * 2, total=0, Hkv=1, ps=2, pages=2) == INV
     assert attn(lib, (1 << 38, 1 << 38, 64) * 2, total=0, Hkv=1, ps=1, pages=1 << 30) == kda.KDA_OK
     assert attn(lib, (1 << 38, 1 << 37, 64) * 2, total=0, Hkv=1, ps=2, pages=1 << 30) == kda.KDA_OK
+
+
+@pytest.mark.parametrize("os,ps,ok", [
+    (9 * 4096, 4096, True), (4096, 2 * 4096, True), (17 * 4096, 2 * 4096, True),
+    (4096, 4096, False), (8 * 4096, 4096, False), (16 * 4096, 2 * 4096, False), (2 * 4096, 2 * 4096, False), (0, 4096, False),
+    (9 * 4096, 4080, False),
+])
+def test_pools_whose_pages_overlap_are_refused(lib, os, ps, ok):
+    """Two layers of nine pages; a list without pairs ends after the checks."""
+    nbytes = lib.kda_pages_compact_workspace_bytes(9)
+    assert copy(lib, os=os, ps=ps, n=0) == (kda.KDA_OK if ok else INV)
+    assert ok or lib.kda_pages_compact_pool(A, 2, os, ps, 4096, 9, A, nbytes, None) == INV
+    # one layer's step, or one page's, says nothing
+    assert copy(lib, os=os, ps=4096, outer=1, n=0) == kda.KDA_OK
+    assert copy(lib, os=9 * 4096, ps=ps, pages=1, n=0) == kda.KDA_OK
