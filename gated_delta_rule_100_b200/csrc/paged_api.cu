@@ -380,6 +380,7 @@ int kda_pages_copy(void *pool, long long outer, long long outer_stride, long lon
                    int num_pages, const int *src, const int *dst, int n, void *stream) {
     if (const int st = pool_check(pool, outer, outer_stride, page_stride, page_bytes, num_pages); st != KDA_OK) return st;
     if (n < 0 || (n > 0 && (!src || !dst))) return KDA_ERR_INVALID_ARG;
+    if (n > kda::PG_MAX_COPY) return KDA_ERR_UNSUPPORTED;
     if (!al(src, 4) || !al(dst, 4)) return KDA_ERR_ALIGNMENT;
     if (n == 0 || outer == 0) return KDA_OK;
     return copy_pages(pool, outer, outer_stride, page_stride, page_bytes, num_pages, src, dst, nullptr, n,

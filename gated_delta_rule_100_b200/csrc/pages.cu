@@ -475,10 +475,70 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
 // took 9 us longer than in 64).  A pair whose destination the list names elsewhere too
 // (as a destination or as a source) is not copied: the others read what was there
 // before the call.
+//
+// Whether a destination is named elsewhere takes a look through the list.  Blocks
+// with few pairs look once a pair; with more than COPY_EACH of them a block looks once
+// for up to COPY_BATCH, their destinations in a hash table in shared memory, so that
+// the work grows with the list and not with its square (once a pair / by batches, us,
+// pages of 4 KB: 2600 pairs 20 / 30, 5000 pairs 38 / 48, 8192 pairs 58 / 69, 16,384
+// pairs 176 / 153, 65,536 pairs 3340 / 680).
 constexpr int COPY_THREADS = 256, COPY_VECS = 16, COPY_UNIT = COPY_THREADS * COPY_VECS * 16;
+constexpr int COPY_EACH = 8;
+enum { CHECK_NONE, CHECK_EACH, CHECK_BATCH };  // a compaction's pairs need none
+constexpr int COPY_BATCH = 1024, COPY_SLOT_BITS = 11, COPY_SLOTS = 1 << COPY_SLOT_BITS;
 
-template <bool CHECK>
+// Destinations, and how often the list names them: open addressing, at most half full.
+struct NamedPages {
+    int page[COPY_SLOTS], times[COPY_SLOTS];
+
+    // the page's slot, or the empty one where it would go
+    __device__ __forceinline__ int slot(int q) const {
+        int at = (int)((uint32_t)q * 0x9e3779b1u >> (32 - COPY_SLOT_BITS));  // by the golden ratio: neighbours part
+        while (page[at] != q && page[at] != -1) at = (at + 1) & (COPY_SLOTS - 1);
+        return at;
+    }
+    // by the whole block: the destinations of pairs [i0, i1) and their count in the list
+    __device__ void fill(const PoolParams &p, int n, int i0, int i1) {
+        __syncthreads();  // the batch before may still be read
+        for (int k = threadIdx.x; k < COPY_SLOTS; k += COPY_THREADS) {
+            page[k] = -1;
+            times[k] = 0;
+        }
+        __syncthreads();
+        for (int i = i0 + threadIdx.x; i < i1; i += COPY_THREADS) {
+            const int q = p.dst[i];
+            if (q < 0 || q >= p.num_pages || p.src[i] == q) continue;  // not copied
+            int at = (int)((uint32_t)q * 0x9e3779b1u >> (32 - COPY_SLOT_BITS));
+            for (;;) {
+                const int was = atomicCAS(&page[at], -1, q);
+                if (was == -1 || was == q) break;
+                at = (at + 1) & (COPY_SLOTS - 1);
+            }
+        }
+        __syncthreads();
+        constexpr int V = 4;
+        for (int j0 = threadIdx.x; j0 < n; j0 += V * COPY_THREADS) {
+            int q[2 * V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int j = j0 + k * COPY_THREADS;
+                q[2 * k] = j < n ? p.dst[j] : -1;
+                q[2 * k + 1] = j < n ? p.src[j] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) {
+                if (q[k] < 0) continue;
+                const int at = slot(q[k]);
+                if (page[at] == q[k]) atomicAdd(&times[at], 1);
+            }
+        }
+        __syncthreads();
+    }
+};
+
+template <int CHECK>
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolParams p) {
+    __shared__ NamedPages named;  // CHECK_BATCH only
     wait_for_primary();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n) : p.n;
     const long long per_page = (p.page_bytes + p.unit - 1) / p.unit, per_pair = per_page * p.outer;
@@ -486,6 +546,7 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolPara
     const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
     int pair = -1, from = 0, to = 0;
     bool ok = false;
+    const int first = (int)(u0 / per_pair), last = u1 > u0 ? (int)((u1 - 1) / per_pair) : first;
     for (long long u = u0; u < u1; ++u) {
         const int i = (int)(u / per_pair);
         if (i != pair) {
@@ -494,14 +555,20 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const PoolPara
             to = p.dst[i];
             ok = from >= 0 && from < p.num_pages && to >= 0 && to < p.num_pages;
             bool bad = !ok && !(from == -1 && to == -1);
-            if constexpr (CHECK) {
+            bool twice = false;
+            if constexpr (CHECK == CHECK_EACH) {
                 if (ok && from != to) {
-                    bool twice = false;
-                    for (int j = threadIdx.x; j < n; j += COPY_THREADS)
-                        twice |= j != i && (p.dst[j] == to || p.src[j] == to) && !(p.src[j] == -1 && p.dst[j] == -1);
-                    if (__syncthreads_or(twice)) { ok = false; bad = true; }
+                    for (int j = threadIdx.x; j < n; j += COPY_THREADS) {
+                        const int a = p.dst[j], b = p.src[j];
+                        twice |= j != i && (a == to || b == to);
+                    }
+                    twice = __syncthreads_or(twice);
                 }
+            } else if constexpr (CHECK == CHECK_BATCH) {
+                if ((i - first) % COPY_BATCH == 0) named.fill(p, n, i, min(i + COPY_BATCH, last + 1));
+                if (ok && from != to) twice = named.times[named.slot(to)] > 1;  // once by the pair itself
             }
+            if (twice) { ok = false; bad = true; }
             if (bad && threadIdx.x == 0) report(p.st, DEV_BAD_ARG);
         }
         if (!ok || from == to) continue;
@@ -579,8 +646,10 @@ cudaError_t launch_pages_copy(PoolParams p, bool check, int sms, cudaStream_t st
     const double each = (double)p.page_bytes * p.outer * p.n / sms;  // bytes an SM
     for (p.unit = COPY_UNIT; p.unit > COPY_UNIT / 8 && p.unit > each; p.unit /= 2) {}
     const long long units = (p.page_bytes + p.unit - 1) / p.unit * p.outer * p.n, top = 8LL * sms;
-    return launch_behind(check ? pages_copy_kernel<true> : pages_copy_kernel<false>, dim3((unsigned)(units < top ? units : top)),
-                         COPY_THREADS, 0, stream, p);
+    const unsigned grid = (unsigned)(units < top ? units : top);
+    auto *kernel = !check ? pages_copy_kernel<CHECK_NONE>
+                   : p.n > (long long)COPY_EACH * grid ? pages_copy_kernel<CHECK_BATCH> : pages_copy_kernel<CHECK_EACH>;
+    return launch_behind(kernel, dim3(grid), COPY_THREADS, 0, stream, p);
 }
 
 }  // namespace kda

@@ -516,7 +516,7 @@ KDA_API int kda_pages_compact_pool(void *pool, long long outer, long long outer_
  * kda_pages_copy -- pages of a pool copied onto others: for every o < outer
  * (layers, keys and values) and i < n, the page_bytes bytes at pool + o *
  * outer_stride + src[i] * page_stride go to the same place of page dst[i].
- * src, dst: int32 [n].  A pair -1, -1 is skipped.  A destination must not be
+ * src, dst: int32 [n], n <= 2^20.  A pair -1, -1 is skipped.  A destination must not be
  * named a second time, as a destination or as a source: such a pair is left
  * out and reported.  pool, page_bytes and the strides (in bytes): multiples of
  * 16; pages do not overlap (those of one o lie inside the step to the next, or

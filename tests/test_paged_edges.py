@@ -79,3 +79,8 @@ def test_pools_whose_pages_overlap_are_refused(lib, os, ps, ok):
     # one layer's step, or one page's, says nothing
     assert copy(lib, os=os, ps=4096, outer=1, n=0) == kda.KDA_OK
     assert copy(lib, os=9 * 4096, ps=ps, pages=1, n=0) == kda.KDA_OK
+
+
+def test_copies_have_a_longest_list(lib):
+    assert copy(lib, n=(1 << 20) + 1) == kda.KDA_ERR_UNSUPPORTED
+    assert copy(lib, n=(1 << 31) - 1) == kda.KDA_ERR_UNSUPPORTED

@@ -72,3 +72,40 @@ def test_pools_that_are_views(layout):
     want[:, [1, 4]] = want[:, [7, 0]]
     kda.pages_copy(pool, ints(7, 0), ints(1, 4))
     assert torch.equal(pool, want) and kda.stream_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("n,outer", [(700, 1), (2600, 1), (5000, 3), (40_000, 1), (300_000, 1)])
+def test_long_copies_leave_out_what_is_named_twice(n, outer):
+    """Lists by which a block copies one pair, some, and more than a batch is: destinations named twice near each other
+    and at the list's two ends, or read elsewhere, pages out of range, pairs skipped and onto themselves."""
+    gen = torch.Generator().manual_seed(n)
+    pages = 2 * n + 50
+    ids = torch.randperm(pages, generator=gen).int()
+    src, dst = ids[:n].clone(), ids[n: 2 * n].clone()
+    src[torch.randint(n, (n // 7,), generator=gen)] = int(src[0])  # a source may be read often
+    dst[n - 1] = dst[1]                                       # written by the first block and by the last
+    dst[n // 2 + 1] = dst[n // 2]
+    src[n // 3] = dst[n // 5]
+    dst[5] = src[5]
+    src[7] = dst[5 + n // 2]                                  # read by one, written by another
+    src[11], dst[11] = -1, -1
+    src[n - 20], dst[n - 20] = -1, -1
+    dst[13], src[17], dst[19] = pages, -1, -1
+    pool = torch.randint(0, 1 << 30, (outer, pages, 4), dtype=torch.int32, generator=gen)
+    want = pool.clone()
+    s, d = src.long(), dst.long()
+    fine = (s >= 0) & (s < pages) & (d >= 0) & (d < pages)
+    times = torch.zeros(pages, dtype=torch.long)
+    times.index_add_(0, d[(d >= 0) & (d < pages)], torch.ones_like(d[(d >= 0) & (d < pages)]))
+    times.index_add_(0, s[(s >= 0) & (s < pages)], torch.ones_like(s[(s >= 0) & (s < pages)]))
+    keep = fine & (s != d) & (times[d.clamp(0, pages - 1)] == 1)
+    assert 0 < int(keep.sum()) < n - 8
+    want[:, d[keep]] = pool[:, s[keep]]
+    x = pool.cuda()
+    kda.pages_copy(x, src.cuda(), dst.cuda())
+    assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
+    assert torch.equal(x.cpu(), want)
+    good = keep.nonzero()[:, 0]
+    x = pool.cuda()
+    kda.pages_copy(x, src[good].cuda(), dst[good].cuda())
+    assert kda.stream_status() == kda.KDA_OK and torch.equal(x.cpu(), want)
