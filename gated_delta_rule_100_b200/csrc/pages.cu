@@ -53,6 +53,7 @@ __device__ __forceinline__ int block_prefix(int v, int *sm, int &total) {
 }
 
 __device__ __forceinline__ int pages_of(int len, int ps) { return (int)(((long long)len + ps - 1) / ps); }
+__device__ __forceinline__ bool length_ok(int len, int P, int ps) { return len >= 0 && pages_of(len, ps) <= P; }
 
 // Marks rows[0..n) in the bitmap; false where one is out of range or marked already.
 // Called by the whole block; needs a barrier before the bitmap is read.
@@ -84,7 +85,8 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagesParams p) {
     for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int row = p.rows[i];
         int *tr = p.table + (long long)row * p.P;
-        const int held = min(pages_of(max(p.length[row], 0), p.ps), p.P);
+        const int len = p.length[row], held = min(pages_of(max(len, 0), p.ps), p.P);
+        if (threadIdx.x == 0 && !length_ok(len, p.P, p.ps)) report(p.st, DEV_BAD_ARG);
         for (int j = threadIdx.x; j < held; j += blockDim.x) {
             const int page = tr[j];
             tr[j] = -1;
@@ -161,7 +163,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
                         ok = false;
                     } else {
                         const int len = p.length[from];
-                        if (len < 0 || pages_of(len, p.ps) > p.P) ok = false;
+                        if (!length_ok(len, p.P, p.ps)) ok = false;
                         else { need = len % p.ps != 0; held = len / p.ps; }
                     }
                 } else {
@@ -259,7 +261,9 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
             p.table[(long long)s_row[lo] * p.P + s_held[lo] + f - s_start[lo]] = page;
             p.ref[page] = 1;
             if constexpr (FORK) {
-                p.copy_src[lo] = p.table[(long long)p.src[lo] * p.P + s_held[lo]];
+                const int came = p.table[(long long)p.src[lo] * p.P + s_held[lo]];
+                if (came < 0 || came >= p.num_pages) report(p.st, DEV_BAD_ARG);
+                p.copy_src[lo] = came;
                 p.copy_dst[lo] = page;
             }
         }
@@ -366,6 +370,7 @@ __device__ __forceinline__ void compact_apply(const PagesParams &p, int n, int m
         const int page = p.table[i];
         int to = page;
         const int len = p.length[row];
+        if (j == 0 && !length_ok(len, p.P, p.ps)) report(p.st, DEV_BAD_ARG);
         if (len > 0 && j < pages_of(len, p.ps)) {
             if (page < 0 || page >= p.num_pages) report(p.st, DEV_BAD_ARG);
             else if (page >= n) {

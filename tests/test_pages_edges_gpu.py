@@ -109,3 +109,46 @@ def test_long_copies_leave_out_what_is_named_twice(n, outer):
     x = pool.cuda()
     kda.pages_copy(x, src[good].cuda(), dst[good].cuda())
     assert kda.stream_status() == kda.KDA_OK and torch.equal(x.cpu(), want)
+
+
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), 33, (1 << 31) - 1])
+def test_lengths_that_cannot_be_are_reported(bad):
+    """By the calls that end or renumber rows too; what the table holds within its bounds is still done."""
+    c = Cache(4, 4, 10, 8)
+    c.reserve([0, 1], [32, 9])
+    t, ln, ref = c.cuda()
+    ln[0] = bad
+    kda.pages_free(t, ln, ref, ints(0), 8)
+    assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
+    assert int(ln[0]) == 0 and int((ref == 0).sum()) == (8 if bad > 0 else 4) and torch.equal(t[1].cpu(), torch.from_numpy(c.table[1]))
+    t, ln, ref = c.cuda()
+    ln[3] = bad
+    t[3] = t[0]  # four live pages, so that the length alone is what is wrong
+    kda.pages_compact(t, ln, ref, 8)
+    assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
+    c.compact()
+    assert torch.equal(t[:2].cpu(), torch.from_numpy(c.table[:2])) and torch.equal(ref.cpu(), torch.from_numpy(c.ref))
+
+
+def test_lengths_of_whole_tables_are_fine():
+    c = Cache(4, 4, 10, 8)
+    c.reserve([0, 1], [32, 25])
+    t, ln, ref = c.cuda()
+    kda.pages_compact(t, ln, ref, 8)
+    c.compact()
+    c.same(t, ln, ref)
+    kda.pages_free(t, ln, ref, ints(0, 1, 2), 8)
+    c.free([0, 1, 2])
+    c.same(t, ln, ref)
+    assert kda.stream_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("page", [-1, 10, 1 << 30, -(1 << 31)])
+def test_a_fork_reports_a_last_page_that_is_none(page):
+    c = Cache(4, 4, 10, 8)
+    c.reserve([0], [12])
+    t, ln, ref = c.cuda()
+    t[0, 1] = page
+    pairs = kda.pages_fork(t, ln, ref, ints(0), ints(2), 8)
+    assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
+    assert pairs.tolist() == [[page], [2]]
