@@ -107,3 +107,65 @@ def test_the_binding_refuses_places_that_overlap():
     assert (flat == 0).all()
     out, lse = call({**c, "kp": good.clone()})
     near(c, out, lse, attention64(c, *appended(c)))
+
+
+@pytest.mark.parametrize("N", [17, 40, 200])
+@pytest.mark.parametrize("append", [True, False])
+def test_chunk_batches_of_many_sequences(N, append):
+    """More sequences than the plan has warps, or a third of its threads; some without tokens, some without a place."""
+    gen = torch.Generator().manual_seed(N)
+    nq = torch.randint(0, 70, (N,), generator=gen).tolist()
+    ln = [t + int(x) for t, x in zip(nq, torch.randint(0, 1500, (N,), generator=gen))]
+    nq[3], ln[3], nq[N // 2], ln[5], nq[N - 1] = 0, 0, 1, max(0, nq[5] - 4), 90
+    ln[N - 1] = 2000
+    c = make(nq, ln, 8, 2, 64, 16, seed=N, span=LONG, permute=True, extra_rows=2)
+    kp, vp = appended(c)
+    if not append:
+        c["kp"].copy_(kp)
+        c["vp"].copy_(vp)
+    lse = torch.full((c["total"], 8), 7.0, device="cuda")
+    new = dict(k_new=c["kn"], v_new=c["vn"]) if append else {}
+    out = kda.paged_attn(c["q"], c["kp"], c["vp"], c["cu"], c["table"], c["length"], c["scale"], max_q=c["max_q"],
+                         rows=c["rows"], lse=lse, **new)
+    assert kda.stream_status() == kda.KDA_OK
+    near(c, out, lse, attention64(c, kp, vp))
+    assert torch.equal(c["kp"].view(torch.int16), kp.view(torch.int16))
+
+
+@pytest.mark.parametrize("nq,ln", [([1500], [3100]), ([700, 300, 1200], [2500, 300, 1600]), ([513] * 12, [513 + 97 * i for i in range(12)])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_items_than_sms(nq, ln, d):
+    """Items that stay whole first, then those that are cut: more of them than SMs, and more partial rows than there is
+    room for in most of the plans that are compared."""
+    c = make(nq, ln, 32, 8, d, 64, seed=sum(nq), span=LONG)
+    tiles = sum(-(-t * 4 // 256) for t in nq)
+    assert tiles * 8 > torch.cuda.get_device_properties(0).multi_processor_count
+    want = attention64(c, *appended(c))
+    out, lse = call(c)
+    assert kda.stream_status() == kda.KDA_OK
+    near(c, out, lse, want)
+    again = call(c)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16)) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("nq,ln", [([1] * 6, [9000, 9, 400, 1, 64, 65]), ([300, 1, 40], [5000, 3000, 41]), ([1], [200])],
+                         ids=["few", "chunk", "whole"])
+def test_calls_in_flight_on_two_streams(nq, ln):
+    """Many calls a stream without a wait between them: workspaces, plans and tickets are each call's own."""
+    span = 0 if ln == [200] else LONG
+    cs = [make(nq, [x + 13 * j * (x > 100) for x in ln], 16, 4, 128, 16, seed=20 + j, span=span) for j in range(2)]
+    want = [attention64(c, *appended(c)) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    calls = 12
+    lses = [[torch.full((c["total"], 16), 7.0, device="cuda") for _ in range(calls)] for c in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(calls):
+        for j, (c, s) in enumerate(zip(cs, streams)):
+            got[j].append(kda.paged_attn(c["q"], c["kp"], c["vp"], c["cu"], c["table"], c["length"], c["scale"],
+                                         max_q=c["max_q"], k_new=c["kn"], v_new=c["vn"], lse=lses[j][i], stream=s))
+    torch.cuda.synchronize()
+    assert kda.stream_status() == kda.KDA_OK
+    for c, outs, ls, w in zip(cs, got, lses, want):
+        for out, lse in zip(outs, ls):
+            near(c, out, lse, w)

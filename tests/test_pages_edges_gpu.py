@@ -1,4 +1,5 @@
 """The pages of a cache: pools, lists and lengths at the edge of what is documented."""
+import numpy as np
 import pytest
 import torch
 
@@ -152,3 +153,34 @@ def test_a_fork_reports_a_last_page_that_is_none(page):
     pairs = kda.pages_fork(t, ln, ref, ints(0), ints(2), 8)
     assert kda.stream_status() == kda.KDA_ERR_INVALID_ARG
     assert pairs.tolist() == [[page], [2]]
+
+
+def test_pools_of_more_pages_than_the_flags_that_are_kept():
+    """300,001 pages are past the first eight steps of a warp, so that the second pass reads counts again; nearly all of
+    them in use, the free ones in runs all over the pool."""
+    c = Cache(1024, 300, 300_001, 2)
+    r = np.random.default_rng(4)
+    t, ln, ref = c.cuda()
+    info = ints(0)
+
+    def reserve(rows, new):
+        kda.pages_reserve(t, ln, ref, ints(*rows), ints(*new), 2, info=info)
+        assert info.item() == c.reserve(rows, new)
+        c.same(t, ln, ref)
+
+    reserve(list(range(1000)), [600 - int(x) for x in r.integers(0, 2, 1000)])
+    for _ in range(2):
+        gone = r.permutation(1000)[:100].tolist()
+        kda.pages_free(t, ln, ref, ints(*gone), 2)
+        c.free(gone)
+        c.same(t, ln, ref)
+        reserve(gone[:60], [int(x) for x in r.integers(0, 601, 60)])
+        src, dst = [k for k in range(1000) if c.length[k]][-40:], gone[60:]
+        pairs = kda.pages_fork(t, ln, ref, ints(*src), ints(*dst), 2, info=info)
+        left, a, b = c.fork(src, dst)
+        assert (info.item(), pairs.tolist()) == (left, [a, b])
+        c.same(t, ln, ref)
+    kda.pages_compact(t, ln, ref, 2, info=info)
+    c.compact()
+    c.same(t, ln, ref)
+    assert kda.stream_status() == kda.KDA_OK
