@@ -88,6 +88,7 @@ struct AttnPlan {
     bool chunk, whole;
     int ctas, entries, tile, sms;
     kda::ChunkLimits lim;
+    int rows;  // of partial sums
     size_t off_entries, off_ml, off_o, bytes;
 };
 AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_size, int P) {
@@ -117,6 +118,7 @@ AttnPlan attn_plan(int N, int total_q, int max_q, int Hq, int Hkv, int d, int pa
         a.entries = a.whole ? 0 : a.ctas;
         rows = a.whole ? 0 : (long long)kda::paged_rows_slots(a.ctas) * a.tile;
     }
+    a.rows = (int)rows;
     a.off_ml = a.off_entries + up256((size_t)a.entries * sizeof(kda::SplitEntry));
     a.off_o = a.off_ml + up256((size_t)rows * sizeof(float2));
     a.bytes = a.whole ? 0 : a.off_o + (size_t)rows * d * sizeof(float);
@@ -271,6 +273,8 @@ int kda_paged_attn(const void *q, const void *k_new, const void *v_new, void *k_
     p.entries = reinterpret_cast<kda::SplitEntry *>(ws + pl.off_entries);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+    p.part_rows = pl.rows;
+    p.max_entries = pl.entries;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == KDA_BF16;
     if (pl.chunk) {

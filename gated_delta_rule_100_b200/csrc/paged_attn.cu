@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
         W += s_sum[w];
     }
     const long long runs = W < grid ? W : grid;  // every run has at least one unit
-    if (!WHOLE && tid == 0) p.entries[c].count = 0;
+    if (!WHOLE && tid == 0 && KDA_CHECK(p.st, c < p.max_entries)) p.entries[c].count = 0;
     if (c >= runs) return;
     long long u = c * W / runs;
     const long long u_end = (c + 1) * W / runs;
@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                 const int pos = lo + i / CH, ch = i % CH, tok = pc.s.q0 + pos - first_new;
                 const int page = p.table[(long long)pc.s.row * p.P + pos / p.page_size], in = pos % p.page_size;
                 if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
+                if (!KDA_CHECK(p.st, tok >= 0 && tok < p.total_q && pos < p.P * p.page_size)) continue;
                 const uint4 kx = *reinterpret_cast<const uint4 *>(p.k_new + tok * p.kn_ts + pc.h * D + ch * 8);
                 const uint4 vx = *reinterpret_cast<const uint4 *>(p.v_new + tok * p.vn_ts + pc.h * D + ch * 8);
                 *reinterpret_cast<uint4 *>(p.kp + page * p.k_ps + in * p.k_ts + pc.h * p.k_hs + ch * 8) = kx;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = pc.t * PA_ROWS + g8 + 8 * e;
-            const bool ok = r < rows;
+            const bool ok = r < rows && KDA_CHECK(p.st, pc.s.q0 + r / G < p.total_q && pc.h < p.Hkv);
             qpos[e] = ok ? first_new + r / G : -1;
             const uint16_t *qr = p.q + (ok ? (pc.s.q0 + r / G) * p.q_ts + (long long)(pc.h * G + r % G) * D : 0);
 #pragma unroll
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
             const float4 a = *reinterpret_cast<const float4 *>(sums + r * S::MSTRIDE + col);
             const int row = done.t * PA_ROWS + r;
             if (begins && ends) {
-                if (row < done.s.nq * G) {
+                if (row < done.s.nq * G && KDA_CHECK(p.st, done.s.q0 + row / G < p.total_q && done.h < p.Hkv)) {
                     const float inv = L == 0.f ? 0.f : 1.f / L;
                     const long long tok = done.s.q0 + row / G;
                     const int head = done.h * G + row % G;
@@ -405,12 +406,12 @@ __global__ void __launch_bounds__(PA_THREADS) paged_rows_kernel(const PagedParam
                     if (p.lse != nullptr && col == 0)
                         p.lse[tok * p.Hq + head] = row_lse(M, L);
                 }
-            } else {
+            } else if (KDA_CHECK(p.st, slot * PA_ROWS + r < p.part_rows)) {
                 *reinterpret_cast<float4 *>(p.part_o + ((long long)slot * PA_ROWS + r) * D + col) = a;
                 if (col == 0) p.part_ml[(long long)slot * PA_ROWS + r] = make_float2(M, L);
             }
         }
-        if (!WHOLE && begins && !ends && tid == 0) {
+        if (!WHOLE && begins && !ends && tid == 0 && KDA_CHECK(p.st, c < p.max_entries)) {
             // runs c + 1 .. last hold the rest: the last is the one with the item's last unit
             const int last = (int)((item_end * runs + W - 1) / W) - 1;
             p.entries[c] = {done.n, done.h, done.t, (grid + c) * PA_ROWS, (c + 1) * PA_ROWS, last - c, PA_ROWS};
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const bool in = k0 + k <= e.count;
-                    const long long x = at(in ? k0 + k : k0);
+                    const long long x0 = at(in ? k0 + k : k0), x = KDA_CHECK(p.st, x0 >= 0 && x0 < p.part_rows) ? x0 : 0;
                     ml[k] = __ldcg(p.part_ml + x);
                     if (!in) ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, in
             const float inv = L == 0.f ? 0.f : 1.f / L;
             const int row = e.t * tile_rows + r, head = e.h * p.G + row % p.G;
             const long long tok = s.q0 + row / p.G;
+            if (!KDA_CHECK(p.st, tok < p.total_q && head < p.Hq)) continue;
 #pragma unroll
             for (int j = 0; j < V; j += 2)
                 *reinterpret_cast<uint32_t *>(p.out + (tok * p.Hq + head) * D + lane * V + j) =

@@ -321,6 +321,7 @@ __device__ void ck_append(const ChunkParams &c, long long first, long long step)
         if (at < 0 || at >= s.nq || pos < 0) continue;
         const int page = p.table[(long long)s.row * p.P + pos / p.page_size], in = pos % p.page_size;
         if (page < 0 || page >= p.num_pages) { report(p.st, DEV_BAD_ARG); continue; }
+        if (!KDA_CHECK(p.st, h < p.Hkv && pos < p.P * p.page_size)) continue;
         const uint4 kx = *reinterpret_cast<const uint4 *>(p.k_new + tok * p.kn_ts + h * D + ch * 8);
         const uint4 vx = *reinterpret_cast<const uint4 *>(p.v_new + tok * p.vn_ts + h * D + ch * 8);
         *reinterpret_cast<uint4 *>(p.kp + page * p.k_ps + in * p.k_ts + h * p.k_hs + ch * 8) = kx;
@@ -772,7 +773,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 nt = pc.kv1 - pc.kv0;
                 if (nt <= 0 || (w == 1 && rows <= CK_M)) continue;
                 idle = w * CK_M + (warp & 3) * 32 >= rows;
-                const bool real = w * CK_M + r < rows;
+                const bool real = w * CK_M + r < rows && KDA_CHECK(p.st, sq.q0 + tok < p.total_q && pc.h < p.Hkv);
                 key0 = pc.kv0 * CK_KT;
                 last = sq.len - sq.nq + tok;
                 if (!real) { last = 0x7ffffff0; m = 0.f; }  // no row: nothing to mask, a reference that never moves
@@ -898,8 +899,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const ChunkPiece pc = c.pieces[at];  // read again: the loop above needs the registers
                 const PagedSeq sq = pc.s;
                 const int row = w * CK_M + r, tok = (pc.t * CK_ROWS + row) / G, head = pc.h * G + (pc.t * CK_ROWS + row) % G;
-                const bool real = row < ck_rows(sq, G, pc.t);
                 const bool whole = pc.part_row < 0;
+                const bool real = row < ck_rows(sq, G, pc.t) && KDA_CHECK(p.st, sq.q0 + tok < p.total_q && head < p.Hq) &&
+                                  KDA_CHECK(p.st, whole || pc.part_row + row < p.part_rows);
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing: 0
                 uint16_t *dst = p.out + ((long long)(sq.q0 + tok) * p.Hq + head) * D;
                 float *part = p.part_o + ((long long)pc.part_row + row) * D;

@@ -39,6 +39,7 @@ struct PagedParams {
     float *part_o;                      // [part rows][d]
     float2 *part_ml;                    // [part rows]
     SplitEntry *entries;
+    int part_rows, max_entries;         // room of the workspace
     DeviceStatus st;
 };
 

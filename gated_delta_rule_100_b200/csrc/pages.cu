@@ -258,6 +258,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
                 }
             }
             // its entries so far come first
+            if (!KDA_CHECK(p.st, lo < p.n && s_held[lo] + f - s_start[lo] < p.P && page < p.num_pages)) continue;
             p.table[(long long)s_row[lo] * p.P + s_held[lo] + f - s_start[lo]] = page;
             p.ref[page] = 1;
             if constexpr (FORK) {
@@ -339,8 +340,8 @@ __global__ void __launch_bounds__(CP_THREADS) compact_rank_kernel(const PagesPar
     for (int k = 0; k < in; ++k) {
         const int q = 4 * i + k;
         const bool live = !(dead >> k & 1u);
-        if (q < n && !live) p.ws_hole[q - lp] = q;
-        if (q >= n && live) {
+        if (q < n && !live && KDA_CHECK(p.st, q >= lp)) p.ws_hole[q - lp] = q;
+        if (q >= n && live && KDA_CHECK(p.st, lp >= below)) {
             p.ws_move[lp - below] = q;
             p.ws_rank[q] = lp - below;
         }
@@ -362,6 +363,7 @@ __device__ __forceinline__ void compact_apply(const PagesParams &p, int n, int m
     }
     for (long long i = me; i < moves; i += all) {
         const int from = p.ws_move[i], to = p.ws_hole[i];
+        if (!KDA_CHECK(p.st, from >= 0 && from < p.num_pages && to >= 0 && to < n)) continue;
         p.ref_out[to] = p.ref[from];
         p.ref_out[from] = 0;
     }
@@ -451,8 +453,8 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
         for (int b = 0; b < 4; ++b) {
             const int q = (k * 32 + lane) * 4 + b;
             const bool is = m >> b & 1u;
-            if (q < n && !is) p.ws_hole[q - at] = q;
-            if (q >= n && is) {
+            if (q < n && !is && KDA_CHECK(p.st, q >= at)) p.ws_hole[q - at] = q;
+            if (q >= n && is && KDA_CHECK(p.st, at >= below)) {
                 p.ws_move[at - below] = q;
                 p.ws_rank[q] = at - below;
             }
