@@ -72,16 +72,23 @@ int attn_sizes(int N, int total_q, int max_q, int Hq, int Hkv, int d, int page_s
 // query heads), and where there are at most kFewUnits 64-key units a CTA, as many as the sizes
 // allow; the chunk kernel otherwise.  Few rows are bound by memory and want many CTAs' loads; the
 // chunk kernel's tiles are 128 rows whatever there is, and its plan, pieces and join take some 12 us.
+// The units are those that the table has room for, as the host reads no lengths: with a table wider
+// than its sequences the chunk kernel comes sooner.  Every figure by units below is for a table as wide
+// as the keys; for 131,072 keys a row they are the chunk kernel's (100 over 3000 26 -> 33 us, 64 over
+// 4000 17 -> 27, 256 over 1024 20 -> 25).  Page sizes that it cannot load (paged_chunk_pages) stay with few
+// rows whatever there is: 2048 tokens over 16,384 keys take 3.7 ms on pages of 48 or 272 tokens, 4.0 ms on
+// pages of 4, and 0.44 on pages of 64.
 // Measured (few rows / chunk kernel, us), 4 key heads of 128, 64 sequences of 128 to 8192 keys: 24
 // rows 81 / 84, 32 rows 83 / 83, 40 rows 132 / 95, 64 rows 143 / 89; of 64: 32 rows 51 / 72, 64 rows
 // 88 / 77.  By units a CTA: 5 (256 tokens over 1024, 8 heads of 64) 21 / 24, 5 (64 over 4000, 4 of 64
-// with 2 queries) 17 / 26, 6 (300 over 1500, 4 of 128) 31 / 31, 7 (512 over 512, 8 of 128) 30 / 28, 8
+// with 2 queries) 17 / 26, 6 (300 over 1500, 4 of 128) 31 / 31, 8 (512 over 512, 8 of 128) 39 / 28, 8
 // (100 over 3000, 2 of 128 with 4) 26 / 33, 9 (16 chunks of 16 over 500) 17 / 25, 11 (200 over 2000, 2
-// of 128 with 4) 33 / 31.
+// of 128 with 4) 33 / 31.  (The units leave out how often rows read their keys again: many rows over
+// few keys are where the rule is off.)
 constexpr int kFewRows = 32, kFewUnits = 9;
 
 // Keys of a full table up to which the kernel of few rows takes items whole: one launch, no join
-// (one token over 257 keys, 4 heads of 64: 7.7 us from 8.9, and a launch less for the host).
+// (one token over 257 keys, 4 heads of 64: 7.8 us from 9.4, and a launch less for the host).
 constexpr int kWholeKeys = 512;
 
 struct AttnPlan {

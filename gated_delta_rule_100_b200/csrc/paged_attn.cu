@@ -11,10 +11,12 @@
 // a step each, and the roundings of many keys average out), while l sums them
 // before that rounding.
 //
-// Bound: HBM.  A key head's keys and values are read once for all its G query
-// heads and new tokens: 4 d bytes per key, against 4 d G n_q operations, far
-// under the card's ratio.  So the kernel is laid out for loads in flight: the
-// rows (tokens x G, at most 16 per item) fill the 16 rows of an mma.sync tile;
+// Bound: HBM.  A key head's keys and values are read once for every 16 of its
+// rows (new tokens times the G query heads): once for up to 16, which is what
+// single tokens are, twice for 17 to 32 (64 sequences of 3 tokens, 8 query heads a
+// key head of 128: 83 us, twice the 41 that one reading takes).  That is 4 d bytes a
+// key against at most 64 d operations, far under the card's ratio.  So the kernel is
+// laid out for loads in flight: the rows of an item, at most 16, fill an mma.sync tile;
 // each of the four warps walks its own 16 keys of every 64 with its own ring of
 // asynchronous 16-byte copies and no block-wide barrier; rows out of the
 // sequence's end are filled with zeros, so whatever lies behind it (NaN too)
@@ -24,7 +26,9 @@
 // tile) items, one run per CTA: lengths from 1 to the cache's end load every SM
 // alike.  An item's own cost counts as PA_HEAD units: for 256 sequences of 128 to
 // 16,384 keys, 8 key heads of 128, the call took 653 us with none, 618, 596, 559
-// and 570 us with 1, 2, 4 and 8; 559 us is 6.6 TB/s, the card's copy rate.  A run
+// and 570 us with 1, 2, 4 and 8.  Those are replays on the same inputs, some of which
+// the L2 cache still holds (3 % of them would fill it); on other inputs each time the
+// call takes 592 to 598 us, 6.2 TB/s, where a plain sum over 4 GB reads 6.5.  A run
 // has at most one item that began before it and one that ends after it; these
 // write their sums to slots, joined by the second kernel in a fixed order (no
 // atomics, so results do not depend on timing).

@@ -20,13 +20,18 @@
 //   reference allows (16-bit rounding is relative and the sums are fp32), so
 //   after the first keys hardly ever.
 // - one weight in sixteen is a polynomial's, which takes work off the exponential
-//   unit.
+//   unit.  (Both this and sums rescaled only past a threshold are published ideas; the
+//   thresholds, the share and the coefficients are this file's own.)
 // - the rows of masked keys behind the sequence's end are zeroed in the last
 //   value tile: a page holds anything there, and 0 x NaN is NaN.
 //
 // Measured, 2048 new tokens over 65,536 keys, 32 query heads, 8 key heads of 128:
-// 1.62 ms = 1340 TFLOP/s, 80 % of a library product's rate in a burst and 94 %
-// of its sustained one.  A 256 x 128 tile takes about 3000 cycles, of which the
+// 1.62 to 1.67 ms a call in a short run, 1300 to 1340 TFLOP/s or 77 to 80 % of a
+// library product's rate in a burst, and 1.91 ms a call in a long one under the power
+// limit, 1130 TFLOP/s or 79 % of that product's sustained rate.  At d = 64, 2048 tokens
+// over 16,384 keys: 698 TFLOP/s, where half the tensor work comes with each
+// exponential (1173 at d = 128; fp16 698 and 1145).  A 256 x 128 tile takes about
+// 3000 cycles at d = 128, of which the
 // tensor cores work 2048: the rest is the way from scores to weights (TMEM load,
 // 2^x, TMEM store and three hand-offs) where a tile's own warps are the only ones
 // that can go on.  Four row tiles would hide it; registers (a row's 64 scores and

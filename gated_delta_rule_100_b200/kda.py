@@ -599,7 +599,8 @@ def paged_attn(q, k_pages, v_pages, cu_q, page_table, length, scale, *, max_q, k
     """Attention of a packed batch of new tokens over a paged cache (see ``kda.h``).
 
     q [total_q,Hq,d] bf16 or fp16, its tokens contiguous or a slice of a wider row; k_pages,
-    v_pages [num_pages,page_size,Hkv,d] of any strides with contiguous channels; cu_q int32
+    v_pages [num_pages,page_size,Hkv,d] of any strides with contiguous channels, under which (where
+    the call writes) places do not overlap; cu_q int32
     [N+1]; page_table int32 [R,P]; length int32 [R], the rows' tokens with the new ones; rows
     int32 [N] or None (rows 0..N-1); max_q the most new tokens that a sequence has.  k_new,
     v_new [total_q,Hkv,d] are written to their pages first; without them the cache holds them.
@@ -772,7 +773,8 @@ def pages_compact(table, length, ref, page_size, *, table_out=None, ref_out=None
 
 def pages_copy(pool, src, dst, *, stream=None):
     """pool[:, dst[i]] = pool[:, src[i]] for int32 [n] src, dst, on a pool [outer, num_pages, ...]
-    with contiguous pages: key/value pages of every layer, or recurrent states in slots."""
+    with contiguous pages: key/value pages of every layer, or recurrent states in slots.
+    At most 2^20 pairs a call."""
     if not _here(pool, stream):
         with _there(pool, stream):
             return pages_copy(pool, src, dst)

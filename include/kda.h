@@ -371,8 +371,12 @@ KDA_API const char *kda_status_string(int status);
  * The models that KDA is for are hybrids: three recurrent layers to one layer
  * of full attention (section 2 of the Baidu breakdown; "The 3:1 Hybrid
  * Architecture" of the "Kimi Linear" explainer).  A server of one keeps, next
- * to the recurrent states, the full-attention layers' keys and values in pages,
- * and reuses both across requests.  A cache is
+ * to the recurrent states, what the full-attention layers remember in pages,
+ * and reuses both across requests.  The page calls serve any such model.  The
+ * attention serves those whose full-attention layers have grouped query heads,
+ * with keys and values of one width; the model that the explainer describes has
+ * latent attention there (one compressed key and value a token, of two widths),
+ * which it does not compute.  A cache is
  *
  *   table  : int32 [R, P]        page numbers; row r is a sequence's slot, its
  *                                first ceil(length[r] / page_size) entries are
@@ -384,9 +388,13 @@ KDA_API const char *kda_status_string(int status);
  * num_pages pages: key and value pages, or the recurrent states themselves (a
  * state [H, dk, dv] in a slot is a page of a pool too).  Calls on one cache
  * must be ordered by the caller (one stream, or events).  What is found bad on
- * the device (a page or row number out of range, a list that names a row
- * twice, a length that does not fit) makes no kernel read or write outside the
- * buffers and is reported by kda_stream_status() as KDA_ERR_INVALID_ARG.
+ * the device (a page or row number out of range, a list of a page call that names
+ * a row twice, a length that does not fit) makes no kernel read or write outside
+ * the buffers and is reported by kda_stream_status() as KDA_ERR_INVALID_ARG.
+ *
+ * These calls alone change lengths and tables.  None of them shortens a row, or
+ * shares less than all of one: a caller who lowers a length by hand loses the
+ * pages behind it, as the next reservation writes over their entries.
  */
 
 /* 16-bit types of kda_paged_attn. */
@@ -431,17 +439,26 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  * reading key head h / (Hq / Hkv).  A position below 0 has no place and no
  * key: nothing is written for it, its out is 0 and its lse -inf.  Products
  * take 16-bit operands (the softmax weights are rounded to dtype, their sum is
- * not) and accumulate in fp32.  Keys and values of positions below length must
- * be finite (a NaN reaches the tokens that see it, a value's perhaps others of
- * its sequence too); whatever pages hold behind them, NaN included, has no
- * effect.
+ * not) and accumulate in fp32; one weight in sixteen of the kernel for chunks is
+ * a polynomial's (relative error 3e-6; 2^-120, in fp16 2^-112, of the row's reference
+ * where it is smaller).  Against 64 bits a result is off by 1.1 to 1.4 times what it would be
+ * with weights in 32 bits.  Keys and values of positions below length must be
+ * finite, and scale q.k within fp32's range (a NaN reaches the tokens that see it,
+ * in out and lse; a value's perhaps others of its sequence too); whatever pages
+ * hold behind them, NaN included, has no effect.  lse is -inf for rows without
+ * keys only.
  * Positions that are written must lie in pages of one row of the call only.
  * Nothing is allocated, so calls can be captured into graphs; lengths, rows and
  * pages may change between replays, sizes may not.
  *
  * Sizes: d in {64, 128}; Hq a multiple of Hkv; any page_size; 1 <= N <= 2^22; pointers
  * to 16-bit data 16-byte aligned and their strides multiples of 8 elements;
- * P * page_size and total_q * Hq below 2^31 - 4096.  total_q == 0 does nothing.
+ * P * page_size and total_q * Hq at most 2^31 - 4096.  total_q == 0 does nothing.
+ *
+ * Chunks are fast on pages of 8, 16, 32, 64 tokens or a multiple of 128.  On any
+ * other size they run on the kernel for few rows, at about an eighth of the speed
+ * (single tokens are as fast on every size).  What a call costs goes by the table's
+ * width too: it chooses between its kernels by the keys that a row has room for.
  */
 KDA_API int kda_paged_attn(const void *q, const void *k_new, const void *v_new,
                   void *k_pages, void *v_pages, const int *cu_q,
@@ -635,7 +652,8 @@ KDA_API int kda_debug_kernel_launches(int *kind, long long *start_ns, long long 
  * points, 102 the packed-batch prefill, the raw-input (fused gate prologue)
  * entry points, the backward pass and the exact-path and two-level test
  * hooks, 103 the host-buffer prefill and the per-launch timing list, 104 the
- * block-reference test hook and the paged cache. */
+ * block-reference test hook.  The paged cache came without a number of its own:
+ * of two libraries of version 104 the one that exports kda_paged_attn has it. */
 KDA_API int kda_abi_version(void);
 
 #ifdef __cplusplus
