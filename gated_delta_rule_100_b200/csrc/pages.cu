@@ -492,7 +492,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
 constexpr int COPY_THREADS = 256, COPY_VECS = 16, COPY_UNIT = COPY_THREADS * COPY_VECS * 16;
 constexpr int COPY_EACH = 8;
 enum { CHECK_NONE, CHECK_EACH, CHECK_BATCH };  // a compaction's pairs need none
-constexpr int COPY_BATCH = 1024, COPY_SLOT_BITS = 11, COPY_SLOTS = 1 << COPY_SLOT_BITS;
+constexpr int COPY_BATCH = 512, COPY_SLOT_BITS = 10, COPY_SLOTS = 1 << COPY_SLOT_BITS;
 
 // Destinations, and how often the list names them: open addressing, at most half full.
 struct NamedPages {

@@ -456,9 +456,10 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  * P * page_size and total_q * Hq at most 2^31 - 4096.  total_q == 0 does nothing.
  *
  * Chunks are fast on pages of 8, 16, 32, 64 tokens or a multiple of 128.  On any
- * other size they run on the kernel for few rows, at about an eighth of the speed
- * (single tokens are as fast on every size).  What a call costs goes by the table's
- * width too: it chooses between its kernels by the keys that a row has room for.
+ * other size they run on the kernel for few rows and take six to nine times as long
+ * (single tokens are as fast on other sizes, and take a sixth longer on the ones
+ * below 8).  What a call costs goes by the table's width too: it chooses between
+ * its kernels by the keys that a row has room for.
  */
 KDA_API int kda_paged_attn(const void *q, const void *k_new, const void *v_new,
                   void *k_pages, void *v_pages, const int *cu_q,
