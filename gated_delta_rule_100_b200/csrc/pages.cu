@@ -488,11 +488,11 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
 // for up to COPY_BATCH, their destinations in a hash table in shared memory, so that
 // the work grows with the list and not with its square (once a pair / by batches, us,
 // pages of 4 KB: 2600 pairs 20 / 30, 5000 pairs 38 / 48, 8192 pairs 58 / 69, 16,384
-// pairs 176 / 153, 65,536 pairs 3340 / 680).
+// pairs 176 / 153, 65,536 pairs 3340 / 680; tables of half the size 155 and 715).
 constexpr int COPY_THREADS = 256, COPY_VECS = 16, COPY_UNIT = COPY_THREADS * COPY_VECS * 16;
 constexpr int COPY_EACH = 8;
 enum { CHECK_NONE, CHECK_EACH, CHECK_BATCH };  // a compaction's pairs need none
-constexpr int COPY_BATCH = 512, COPY_SLOT_BITS = 10, COPY_SLOTS = 1 << COPY_SLOT_BITS;
+constexpr int COPY_BATCH = 1024, COPY_SLOT_BITS = 11, COPY_SLOTS = 1 << COPY_SLOT_BITS;
 
 // Destinations, and how often the list names them: open addressing, at most half full.
 struct NamedPages {

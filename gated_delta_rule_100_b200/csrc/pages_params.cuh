@@ -8,7 +8,7 @@
 namespace kda {
 
 constexpr int PG_MAX_ROWS = 65536;  // rows of a table: a bit each in shared memory
-constexpr int PG_MAX_COPY = 1 << 20;  // pairs of one copy: every block looks through them once (up to a batch of pairs a block)
+constexpr int PG_MAX_COPY = 1 << 21;  // pairs of one copy: every block looks through them all, once for each 1024 of its own
 constexpr int PG_MAX_LIST = 8192;   // sequences of one reserve or fork: their prefix sums lie in shared memory
 
 struct PagesParams {

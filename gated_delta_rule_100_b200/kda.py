@@ -774,7 +774,7 @@ def pages_compact(table, length, ref, page_size, *, table_out=None, ref_out=None
 def pages_copy(pool, src, dst, *, stream=None):
     """pool[:, dst[i]] = pool[:, src[i]] for int32 [n] src, dst, on a pool [outer, num_pages, ...]
     with contiguous pages: key/value pages of every layer, or recurrent states in slots.
-    At most 2^20 pairs a call."""
+    At most 2^21 pairs a call."""
     if not _here(pool, stream):
         with _there(pool, stream):
             return pages_copy(pool, src, dst)

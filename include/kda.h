@@ -440,13 +440,13 @@ enum { KDA_BF16 = 0, KDA_FP16 = 1 };
  * key: nothing is written for it, its out is 0 and its lse -inf.  Products
  * take 16-bit operands (the softmax weights are rounded to dtype, their sum is
  * not) and accumulate in fp32; one weight in sixteen of the kernel for chunks is
- * a polynomial's (relative error 3e-6; 2^-120, in fp16 2^-112, of the row's reference
- * where it is smaller).  Against 64 bits a result is off by 1.1 to 1.4 times what it would be
- * with weights in 32 bits.  Keys and values of positions below length must be
- * finite, and scale q.k within fp32's range (a NaN reaches the tokens that see it,
- * in out and lse; a value's perhaps others of its sequence too); whatever pages
- * hold behind them, NaN included, has no effect.  lse is -inf for rows without
- * keys only.
+ * a polynomial's (relative error 3e-6; 2^-120, in fp16 2^-112, of the row's
+ * reference where it is smaller).  A result is off by 1.1 to 1.4 times what it
+ * would be with weights in 32 bits.  Keys and values of positions below length
+ * must be finite, and scale q.k within fp32's range (a NaN reaches the tokens that
+ * see it, in out and lse; a value's perhaps others of its sequence too); whatever
+ * pages hold behind them, NaN included, has no effect.  lse is -inf for rows
+ * without keys only.
  * Positions that are written must lie in pages of one row of the call only.
  * Nothing is allocated, so calls can be captured into graphs; lengths, rows and
  * pages may change between replays, sizes may not.
@@ -534,7 +534,7 @@ KDA_API int kda_pages_compact_pool(void *pool, long long outer, long long outer_
  * kda_pages_copy -- pages of a pool copied onto others: for every o < outer
  * (layers, keys and values) and i < n, the page_bytes bytes at pool + o *
  * outer_stride + src[i] * page_stride go to the same place of page dst[i].
- * src, dst: int32 [n], n <= 2^20.  A pair -1, -1 is skipped.  A destination must not be
+ * src, dst: int32 [n], n <= 2^21.  A pair -1, -1 is skipped.  A destination must not be
  * named a second time, as a destination or as a source: such a pair is left
  * out and reported.  pool, page_bytes and the strides (in bytes): multiples of
  * 16; pages do not overlap (those of one o lie inside the step to the next, or

@@ -82,5 +82,5 @@ def test_pools_whose_pages_overlap_are_refused(lib, os, ps, ok):
 
 
 def test_copies_have_a_longest_list(lib):
-    assert copy(lib, n=(1 << 20) + 1) == kda.KDA_ERR_UNSUPPORTED
+    assert copy(lib, n=(1 << 21) + 1) == kda.KDA_ERR_UNSUPPORTED
     assert copy(lib, n=(1 << 31) - 1) == kda.KDA_ERR_UNSUPPORTED
